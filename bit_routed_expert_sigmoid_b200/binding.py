@@ -27,6 +27,14 @@ FLINT_W_NVFP4 = 1
 FLINT_FLAG_DEBUG_CHECKS = 0x1
 FLINT_FLAG_W4A4 = 0x2
 
+FLINT_T_BF16 = 0
+FLINT_T_F16 = 1
+FLINT_T_F32 = 2
+FLINT_ACT_NONE = 0
+FLINT_ACT_SWIGLU = 1
+FLINT_GATE_NONE = 0
+FLINT_GATE_SIGMOID = 1
+
 FLINT_BUF_LOGITS = 0
 FLINT_BUF_XQ = 1
 FLINT_BUF_YS = 2
@@ -45,6 +53,7 @@ EXPORTS = (
     "flint_moe_status_string", "flint_moe_set_stage_events", "flint_moe_stage_count", "flint_moe_stage_name",
     "flint_moe_route_noalloc", "flint_residual_rmsnorm", "flint_moe_stack_forward",
     "flint_quantize_int4_g128", "flint_quantize_nvfp4",
+    "flint_q4_linear", "flint_grouped_linear", "flint_expert_permute", "flint_expert_combine", "flint_block_norm",
 )
 
 
@@ -66,12 +75,20 @@ class flint_moe_weights(ctypes.Structure):
                                                 "dn_scales", "dn_tscale", "sh_gu", "sh_dn")]
 
 
+class flint_norm_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "x_out", "y", "gate", "post_weight", "pre_weight", "z")]
+                + [(n, ctypes.c_longlong) for n in ("ldx", "ldxo", "ldy", "ldg", "ldz")]
+                + [(n, ctypes.c_int) for n in ("T", "H", "type", "res_type", "w_type", "post_norm", "gate_act")]
+                + [(n, ctypes.c_float) for n in ("res_scale", "branch_scale", "eps")])
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m bit_routed_expert_sigmoid_b200.build` "
                           "(the Flint MoE layer has no implementation other than its CUDA kernels)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, V = ctypes.POINTER, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+    L, F = ctypes.c_longlong, ctypes.c_float
     sig = {
         "flint_moe_workspace_size": (S, [P(flint_moe_cfg)]),
         "flint_moe_create": (I, [P(flint_moe_cfg), P(flint_moe_weights), V, S, P(V)]),
@@ -96,6 +113,11 @@ def _load():
         "flint_moe_stack_forward": (I, [P(V), I, V, I, ctypes.c_float, V, V, V]),
         "flint_quantize_int4_g128": (I, [V, ctypes.c_longlong, I, I, V, V, V]),
         "flint_quantize_nvfp4": (I, [V, I, I, I, V, V, V, V]),
+        "flint_q4_linear": (I, [I, I, I, I, V, V, V, V, L, I, I, V, L, V]),
+        "flint_grouped_linear": (I, [I, I, I, I, I, V, V, L, I, V, I, V, I, V, L, V]),
+        "flint_expert_permute": (I, [V, I, I, I, V, V, V, V]),
+        "flint_expert_combine": (I, [V, L, I, V, V, I, I, I, F, V, L, I, V, L, V]),
+        "flint_block_norm": (I, [P(flint_norm_args), V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -217,6 +239,33 @@ def flint_quantize_nvfp4(w: int, n_mats: int, rows: int, cols: int, codes: int, 
     _check(_lib.flint_quantize_nvfp4(ctypes.c_void_p(w), int(n_mats), int(rows), int(cols), ctypes.c_void_p(codes),
                                      ctypes.c_void_p(scales), ctypes.c_void_p(tscale), ctypes.c_void_p(stream)),
            "flint_quantize_nvfp4")
+
+
+def flint_q4_linear(fmt: int, N: int, K: int, rotated: int, codes: int, scales: int, tscale: int, x: int, ldx: int,
+                    T: int, type: int, y: int, ldy: int, stream: int = 0) -> None:
+    _check(_lib.flint_q4_linear(fmt, N, K, rotated, codes, scales, tscale, x, ldx, T, type, y, ldy, stream),
+           "flint_q4_linear")
+
+
+def flint_grouped_linear(E: int, N: int, K: int, act: int, type: int, w: int, x: int, ldx: int, x_rows: int, row_of: int,
+                         row_div: int, offsets: int, P: int, y: int, ldy: int, stream: int = 0) -> None:
+    _check(_lib.flint_grouped_linear(E, N, K, act, type, w, x, ldx, x_rows, row_of, row_div, offsets, P, y, ldy, stream),
+           "flint_grouped_linear")
+
+
+def flint_expert_permute(ids: int, T: int, top_k: int, E: int, offsets: int, perm: int, inv: int,
+                         stream: int = 0) -> None:
+    _check(_lib.flint_expert_permute(ids, T, top_k, E, offsets, perm, inv, stream), "flint_expert_permute")
+
+
+def flint_expert_combine(o: int, ldo: int, P: int, inv: int, w: int, T: int, top_k: int, H: int, scale: float, addend: int,
+                         lda: int, type: int, y: int, ldy: int, stream: int = 0) -> None:
+    _check(_lib.flint_expert_combine(o, ldo, P, inv, w, T, top_k, H, scale, addend, lda, type, y, ldy, stream),
+           "flint_expert_combine")
+
+
+def flint_block_norm(args: flint_norm_args, stream: int = 0) -> None:
+    _check(_lib.flint_block_norm(ctypes.byref(args), stream), "flint_block_norm")
 
 
 def flint_moe_destroy(h: int) -> None:

@@ -1,0 +1,241 @@
+// Around the products grouped by expert: the expert-major permutation of (token, slot) pairs and the weighted
+// combination of the experts' rows (flint_expert_permute, flint_expert_combine).
+#include <cooperative_groups.h>
+
+#include "kernels.cuh"
+#include "ops.cuh"
+
+namespace flint {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+// ---------------------------------------------------------------------------------------------
+// Permutation: a counting sort that keeps pair order, in one launch of one cluster. Warp g of the cluster owns
+// the pairs [g wlen, (g+1) wlen). It counts its pairs per expert in its own row of shared memory (counts do not
+// depend on the order of the adds); the exclusive scans over the warps of a CTA, the CTAs of the cluster (read
+// through distributed shared memory) and the experts then give each (warp, expert) its first position, and the
+// warp hands out positions 32 pairs at a time by rank among equal ids (match.any). Deterministic throughout.
+constexpr int kPermMaxCtas = 8;                  // portable cluster size
+constexpr int kPermMaxThreads = 1024;
+
+__device__ __forceinline__ int pad32(int i) { return i + (i >> 5); }
+
+__global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const int* __restrict__ ids, int P, int E,
+                                                                         int wlen, int* __restrict__ offsets,
+                                                                         int* __restrict__ perm, int* __restrict__ inv) {
+  extern __shared__ int sm_perm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  int* tot = sm_perm;                            // [pad32(E) + 1] this CTA's pairs per expert
+  int* first = tot + pad32(E) + 1;               // [pad32(E) + 1] cluster totals, then first positions
+  int* cnt = first + pad32(E) + 1;               // [nw][E]
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = static_cast<int>(cl.block_rank()), ncta = static_cast<int>(cl.num_blocks());
+
+  for (int i = threadIdx.x; i < nw * E; i += blockDim.x) cnt[i] = 0;
+  __syncthreads();
+  const long long lo_ll = static_cast<long long>(rank * nw + warp) * wlen;
+  const int lo = static_cast<int>(min(lo_ll, static_cast<long long>(P)));
+  const int hi = static_cast<int>(min(lo_ll + wlen, static_cast<long long>(P)));
+  int* mine = cnt + warp * E;
+  for (int i0 = lo; i0 < hi; i0 += 128) {
+    int v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i0 + 32 * u + lane < hi ? __ldg(ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (v[u] >= 0 && v[u] < E) atomicAdd(mine + v[u], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int run = 0;
+    for (int w = 0; w < nw; ++w) {
+      const int c = cnt[w * E + e];
+      cnt[w * E + e] = run;
+      run += c;
+    }
+    tot[pad32(e)] = run;
+  }
+  cl.sync();
+  // cluster totals per expert, and the pairs that CTAs before this one hold
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int all = 0, before = 0;
+    for (int c = 0; c < ncta; ++c) {
+      const int v = cl.map_shared_rank(tot, c)[pad32(e)];
+      if (c < rank) before += v;
+      all += v;
+    }
+    first[pad32(e)] = all;
+    for (int w = 0; w < nw; ++w) cnt[w * E + e] += before;
+  }
+  cl.sync();                                     // also: nobody reads another CTA's memory behind this
+  if (warp == 0) {                               // exclusive scan over the experts, E/32 neighbours per lane
+    const int per = (E + 31) / 32;
+    int s = 0;
+    for (int j = 0; j < per; ++j)
+      if (lane * per + j < E) s += first[pad32(lane * per + j)];
+    int incl = s;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+      if (lane >= m) incl += o;
+    }
+    int run = incl - s;
+    for (int j = 0; j < per; ++j) {
+      const int e = lane * per + j;
+      if (e < E) {
+        const int c = first[pad32(e)];
+        first[pad32(e)] = run;
+        run += c;
+      }
+    }
+    if (lane == 31) first[pad32(E)] = run;
+  }
+  __syncthreads();
+  if (rank == 0)
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = first[pad32(e)];
+  for (int i0 = lo; i0 < hi; i0 += 128) {
+    int v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i0 + 32 * u + lane < hi ? __ldg(ids + i0 + 32 * u + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 32 * u + lane;
+      const int e = v[u] >= 0 && v[u] < E ? v[u] : -1;
+      const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+      const int r = __popc(peers & ((1u << lane) - 1u));
+      int pos = -1;
+      if (e >= 0) pos = first[pad32(e)] + mine[e] + r;
+      __syncwarp();
+      if (e >= 0 && r == 0) mine[e] += __popc(peers);
+      __syncwarp();
+      if (i < hi) {
+        inv[i] = pos;
+        if (pos >= 0) perm[pos] = i;
+      }
+    }
+  }
+  for (long long i = static_cast<long long>(first[pad32(E)]) + rank * blockDim.x + threadIdx.x; i < P;
+       i += static_cast<long long>(ncta) * blockDim.x)
+    perm[i] = -1;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Combination: y[t] = scale * sum_k w[t][k] o[inv[t][k]] + addend[t]. HBM-bound: every kept row of o is read
+// once. A thread owns 8 columns (16-byte accesses) or one (any alignment), and issues the loads of 8 slots
+// before their sum, which runs in slot order.
+template <int TYPE, bool VEC>
+__global__ void __launch_bounds__(256) expert_combine_kernel(const __grid_constant__ CombineParams p) {
+  constexpr int kCols = VEC ? 8 : 1;
+  const long long t = blockIdx.x;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kCols;
+  if (c >= p.H) return;
+  float acc[kCols];
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
+  for (int k0 = 0; k0 < p.top_k; k0 += 8) {
+    int row[8];
+    float wk[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = k0 + k < p.top_k;
+      row[k] = in ? __ldg(p.inv + t * p.top_k + k0 + k) : -1;
+      wk[k] = in ? __ldg(p.w + t * p.top_k + k0 + k) : 0.f;
+      if (row[k] >= p.P) row[k] = -1;
+    }
+    if constexpr (VEC) {
+      uint4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (row[k] >= 0) v[k] = __ldg(reinterpret_cast<const uint4*>(p.o + row[k] * p.ldo + c));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (row[k] < 0) continue;
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = pair_to_f32<TYPE>(w[j]);
+          acc[2 * j] = fmaf(wk[k], f.x, acc[2 * j]);
+          acc[2 * j + 1] = fmaf(wk[k], f.y, acc[2 * j + 1]);
+        }
+      }
+    } else {
+      uint16_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (row[k] >= 0) v[k] = __ldg(p.o + row[k] * p.ldo + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (row[k] >= 0) acc[0] = fmaf(wk[k], to_f32<TYPE>(v[k]), acc[0]);
+    }
+  }
+  if constexpr (VEC) {
+    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (p.addend) {                              // may be y itself: an ordinary load
+      const uint4 r = *reinterpret_cast<const uint4*>(p.addend + t * p.lda + c);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = pair_to_f32<TYPE>(w[j]);
+        a[2 * j] = f.x;
+        a[2 * j + 1] = f.y;
+      }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = pair_from_f32<TYPE>(fmaf(p.scale, acc[2 * j], a[2 * j]), fmaf(p.scale, acc[2 * j + 1], a[2 * j + 1]));
+    *reinterpret_cast<uint4*>(p.y + t * p.ldy + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    const float a = p.addend ? to_f32<TYPE>(p.addend[t * p.lda + c]) : 0.f;
+    p.y[t * p.ldy + c] = from_f32<TYPE>(fmaf(p.scale, acc[0], a));
+  }
+}
+
+template <int TYPE>
+cudaError_t launch_combine_type(const CombineParams& p, cudaStream_t s) {
+  auto ok = [](const void* q, long long ld) {
+    return !q || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0);
+  };
+  const bool vec = p.H % 8 == 0 && ok(p.o, p.ldo) && ok(p.addend, p.lda) && ok(p.y, p.ldy);
+  const int units = vec ? p.H / 8 : p.H;
+  const int threads = units >= 256 ? 256 : (units + 31) / 32 * 32;
+  const dim3 grid(p.T, (units + threads - 1) / threads);
+  if (grid.y > 65535) return cudaErrorInvalidConfiguration;
+  if (vec) expert_combine_kernel<TYPE, true><<<grid, threads, 0, s>>>(p);
+  else expert_combine_kernel<TYPE, false><<<grid, threads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, int* perm, int* inv, cudaStream_t s) {
+  const int ncta = P <= 4096 ? 1 : kPermMaxCtas;
+  int threads = ((P + ncta - 1) / ncta + 31) / 32 * 32;
+  threads = threads < 256 ? 256 : threads > kPermMaxThreads ? kPermMaxThreads : threads;
+  const int warps = ncta * (threads / 32);
+  const int wlen = ((P + warps - 1) / warps + 31) / 32 * 32;
+  const int smem = 4 * (2 * (E + E / 32 + 1) + threads / 32 * E);
+  cudaError_t e = cudaFuncSetAttribute(expert_permute_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ncta);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ncta;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, expert_permute_kernel, ids, P, E, wlen, offsets, perm, inv);
+}
+
+cudaError_t launch_expert_combine(const CombineParams& p, cudaStream_t s) {
+  return p.type == kTBf16 ? launch_combine_type<kTBf16>(p, s) : launch_combine_type<kTF16>(p, s);
+}
+
+}  // namespace flint

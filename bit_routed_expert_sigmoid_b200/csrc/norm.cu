@@ -1,0 +1,218 @@
+// The residual step around a block (flint_block_norm): post-norm of the branch, gate, residual add and the
+// next block's pre-norm in one pass, every row read once and held in registers between the two reductions.
+#include "kernels.cuh"
+#include "ops.cuh"
+
+namespace flint {
+
+namespace {
+
+constexpr int kNormWarps = 32;
+
+// Sum over the CTA in a fixed order: the warp butterfly, then the warps in order.
+__device__ __forceinline__ float block_sum(float v, float* wsum) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) wsum[warp] = v;
+  __syncthreads();
+  float tot = 0.f;
+  for (int w = 0; w < nw; ++w) tot += wsum[w];
+  return tot;
+}
+
+// Element k (of 8 VPT) of a thread: 8 neighbours per step with 16-byte accesses, else one element per step so
+// that a warp's accesses are neighbours.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int k) {
+  if constexpr (VEC) return ((k >> 3) * blockDim.x + threadIdx.x) * 8 + (k & 7);
+  else return k * blockDim.x + threadIdx.x;
+}
+
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void load8(const uint16_t* row, int v, int H, float (&out)[8]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(8 * v);
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (c < H) r = *reinterpret_cast<const uint4*>(row + c);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = pair_to_f32<TYPE>(w[j]);
+      out[2 * j] = f.x;
+      out[2 * j + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = col_of<false>(8 * v + j);
+      out[j] = c < H ? to_f32<TYPE>(row[c]) : 0.f;
+    }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8_f32(const float* row, int v, int H, float (&out)[8]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(8 * v);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (c < H) {
+      a = *reinterpret_cast<const float4*>(row + c);
+      b = *reinterpret_cast<const float4*>(row + c + 4);
+    }
+    out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
+    out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = col_of<false>(8 * v + j);
+      out[j] = c < H ? row[c] : 0.f;
+    }
+  }
+}
+
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void store8(uint16_t* row, int v, int H, const float (&in)[8]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(8 * v);
+    if (c < H)
+      *reinterpret_cast<uint4*>(row + c) =
+          make_uint4(pair_from_f32<TYPE>(in[0], in[1]), pair_from_f32<TYPE>(in[2], in[3]),
+                     pair_from_f32<TYPE>(in[4], in[5]), pair_from_f32<TYPE>(in[6], in[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = col_of<false>(8 * v + j);
+      if (c < H) row[c] = from_f32<TYPE>(in[j]);
+    }
+  }
+}
+
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void load8_weight(const void* w, int w_f32, int v, int H, float (&out)[8]) {
+  if (w_f32) load8_f32<VEC>(static_cast<const float*>(w), v, H, out);
+  else load8<TYPE, VEC>(static_cast<const uint16_t*>(w), v, H, out);
+}
+
+template <int TYPE, bool RES_F32, bool VEC, int VPT>
+__global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sum_post[kNormWarps], sum_pre[kNormWarps];
+  const long long t = blockIdx.x;
+  const int H = p.H;
+  float x[VPT][8], b[VPT][8];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if constexpr (RES_F32) load8_f32<VEC>(static_cast<const float*>(p.x) + t * p.ldx, v, H, x[v]);
+    else load8<TYPE, VEC>(static_cast<const uint16_t*>(p.x) + t * p.ldx, v, H, x[v]);
+  }
+  if (p.y) {
+    float g[VPT][8];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) load8<TYPE, VEC>(p.y + t * p.ldy, v, H, b[v]);
+    if (p.gate) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) load8<TYPE, VEC>(p.gate + t * p.ldg, v, H, g[v]);
+    }
+    if (p.post_norm) {
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(b[v][j], b[v][j], s);
+      const float inv = 1.0f / sqrtf(block_sum(s, sum_post) / static_cast<float>(H) + p.eps);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        float w[8];
+        if (p.post_w) load8_weight<TYPE, VEC>(p.post_w, p.w_f32, v, H, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[v][j] = b[v][j] * inv * (p.post_w ? w[j] : 1.0f);
+      }
+    }
+    if (p.gate) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          b[v][j] *= p.gate_act == 1 ? 1.0f / (1.0f + expf(-g[v][j])) : g[v][j];
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] = fmaf(p.branch_scale, b[v][j], p.res_scale * x[v][j]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] *= p.res_scale;
+  }
+  if (p.x_out) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if constexpr (RES_F32) {
+        float* row = static_cast<float*>(p.x_out) + t * p.ldxo;
+        if constexpr (VEC) {
+          const int c = col_of<true>(8 * v);
+          if (c < H) {
+            *reinterpret_cast<float4*>(row + c) = make_float4(x[v][0], x[v][1], x[v][2], x[v][3]);
+            *reinterpret_cast<float4*>(row + c + 4) = make_float4(x[v][4], x[v][5], x[v][6], x[v][7]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = col_of<false>(8 * v + j);
+            if (c < H) row[c] = x[v][j];
+          }
+        }
+      } else {
+        store8<TYPE, VEC>(static_cast<uint16_t*>(p.x_out) + t * p.ldxo, v, H, x[v]);
+      }
+    }
+  }
+  if (!p.z) return;
+  float s = 0.f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(x[v][j], x[v][j], s);   // columns behind H hold zeros
+  const float inv = 1.0f / sqrtf(block_sum(s, sum_pre) / static_cast<float>(H) + p.eps);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    float w[8];
+    if (p.pre_w) load8_weight<TYPE, VEC>(p.pre_w, p.w_f32, v, H, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[v][j] = x[v][j] * inv * (p.pre_w ? w[j] : 1.0f);
+    store8<TYPE, VEC>(p.z + t * p.ldz, v, H, x[v]);
+  }
+}
+
+template <int TYPE, bool RES_F32, bool VEC>
+cudaError_t launch_vpt(const NormParams& p, cudaStream_t s) {
+  const int n8 = (p.H + 7) / 8;
+  const int vpt = n8 <= 1024 ? 1 : n8 <= 2048 ? 2 : 4;
+  const int threads = ((n8 + vpt - 1) / vpt + 31) / 32 * 32;
+  if (vpt == 1) block_norm_kernel<TYPE, RES_F32, VEC, 1><<<p.T, threads, 0, s>>>(p);
+  else if (vpt == 2) block_norm_kernel<TYPE, RES_F32, VEC, 2><<<p.T, threads, 0, s>>>(p);
+  else block_norm_kernel<TYPE, RES_F32, VEC, 4><<<p.T, threads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int TYPE>
+cudaError_t launch_type(const NormParams& p, cudaStream_t s) {
+  // 16-byte accesses where every row of every operand starts on 16 bytes
+  const long long re = p.res_f32 ? 4 : 8;
+  auto ok = [](const void* q, long long ld, long long e) {
+    return !q || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % e == 0);
+  };
+  const bool vec = p.H % 8 == 0 && ok(p.x, p.ldx, re) && ok(p.x_out, p.ldxo, re) && ok(p.y, p.ldy, 8) &&
+                   ok(p.gate, p.ldg, 8) && ok(p.z, p.ldz, 8) && ok(p.post_w, 0, 8) && ok(p.pre_w, 0, 8);
+  if (p.res_f32) return vec ? launch_vpt<TYPE, true, true>(p, s) : launch_vpt<TYPE, true, false>(p, s);
+  return vec ? launch_vpt<TYPE, false, true>(p, s) : launch_vpt<TYPE, false, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s) {
+  return p.type == kTBf16 ? launch_type<kTBf16>(p, s) : launch_type<kTF16>(p, s);
+}
+
+}  // namespace flint

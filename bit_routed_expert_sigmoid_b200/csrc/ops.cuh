@@ -1,0 +1,92 @@
+// Kernel launchers of the standalone operators (internal interface between ops_api.cu and the device code).
+#pragma once
+
+#include "common.cuh"
+
+namespace flint {
+
+enum OpType : int { kTBf16 = 0, kTF16 = 1, kTF32 = 2 };
+
+struct Q4Params {
+  int fmt, N, K, rotated;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* tscale;
+  const uint16_t* x;
+  long long ldx;
+  int T, type;
+  uint16_t* y;
+  long long ldy;
+};
+cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s);
+
+struct GroupedParams {
+  int E, N, K, act, type;
+  const uint16_t* w;
+  const uint16_t* x;
+  long long ldx;
+  int x_rows;
+  const int* row_of;
+  int row_div;
+  const int* offsets;
+  int P;
+  uint16_t* y;
+  long long ldy;
+};
+cudaError_t launch_grouped_linear(const GroupedParams& p, cudaStream_t s);
+
+cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, int* perm, int* inv, cudaStream_t s);
+
+struct CombineParams {
+  const uint16_t* o;
+  long long ldo;
+  int P;
+  const int* inv;
+  const float* w;
+  int T, top_k, H;
+  float scale;
+  const uint16_t* addend;
+  long long lda;
+  int type;
+  uint16_t* y;
+  long long ldy;
+};
+cudaError_t launch_expert_combine(const CombineParams& p, cudaStream_t s);
+
+struct NormParams {
+  const void* x;
+  void* x_out;
+  const uint16_t* y;
+  const uint16_t* gate;
+  const void* post_w;
+  const void* pre_w;
+  uint16_t* z;
+  long long ldx, ldxo, ldy, ldg, ldz;
+  int T, H, type, res_f32, w_f32, post_norm, gate_act;
+  float res_scale, branch_scale, eps;
+};
+cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s);
+
+// 16-bit element of an activation tensor as fp32, and back (one rounding, to nearest even)
+template <int TYPE>
+__device__ __forceinline__ float to_f32(uint16_t b) {
+  if constexpr (TYPE == kTBf16) return bf16_bits_to_f32(b);
+  else return __half2float(__ushort_as_half(b));
+}
+template <int TYPE>
+__device__ __forceinline__ uint16_t from_f32(float f) {
+  if constexpr (TYPE == kTBf16) return f32_to_bf16_bits(f);
+  else return __half_as_ushort(__float2half_rn(f));
+}
+template <int TYPE>
+__device__ __forceinline__ float2 pair_to_f32(uint32_t w) {
+  if constexpr (TYPE == kTBf16) return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t pair_from_f32(float lo, float hi) {
+  if constexpr (TYPE == kTBf16) return pack_bf162(lo, hi);
+  else return pack_half2(lo, hi);
+}
+
+}  // namespace flint

@@ -1,0 +1,501 @@
+"""The standalone operators on the GPU against their fp64 oracle (oracle/ops_ref.py).
+
+Tolerances. An output of type t carries one rounding: u_t |ref| with u_t half a step (bf16 2^-8, fp16 2^-11),
+plus half the smallest subnormal step of fp16. Before it, an fp32 sum of n products taken in any order with
+intermediate rounding is within n 2^-23 of sum |w x| (2^-24 per addition, doubled because the tensor cores may
+truncate); the kernels add 16 products per step at least and join at most 64 partial sums, so n = K/16 + 80.
+Rotated activations are rounded once to 16 bits of at least fp16's precision per element: 2^-11 of sum |w' x'|
+more. Over a whole output the roundings are independent, so the error's norm stays below (u_t + 2^-11 if rotated)
+times the result's norm, a bound that a wrong element or group breaks at once."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU-only machines, skipped there
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from bit_routed_expert_sigmoid_b200 import binding as B  # noqa: E402
+from bit_routed_expert_sigmoid_b200 import ops  # noqa: E402
+from oracle import flint_moe_ref as R  # noqa: E402
+from oracle import ops_ref as O  # noqa: E402
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TYPES = [torch.bfloat16, torch.float16]
+
+
+def f64(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def close(got, ref, dtype, slack=0.0, norm_extra=0.0, rows=None):
+    got, ref = f64(got), np.asarray(ref)
+    if rows is not None:
+        got, ref, slack = got[rows], ref[rows], (slack[rows] if isinstance(slack, np.ndarray) else slack)
+    assert np.isfinite(got).all()
+    err = np.abs(got - ref)
+    tol = U[dtype] * (np.abs(ref) + slack) + slack + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    assert np.all(err <= tol), float((err / np.maximum(tol, 1e-300)).max())
+    norm = np.linalg.norm(ref)
+    assert np.linalg.norm(err) <= (U[dtype] + norm_extra + 2.0 ** -20) * norm + 2.0 ** -25 * np.sqrt(ref.size)
+
+
+# ------------------------------------------------------------------------------------------ 4-bit linear
+
+def q4_case(fmt, N, K, T, dtype, seed, pad=0, hot=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, K + pad), generator=g) * 1.26
+    if hot:
+        x[:, torch.randint(0, K, (1 + K // 512,), generator=g)] *= 50.0
+    x = x.to(dtype).cuda()[:, :K]
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    if fmt == "int4":
+        scales = (torch.randn((N, K // 128), generator=g) * 0.01).to(torch.bfloat16)
+        ts = None
+    else:
+        scales = (torch.randn((N, K // 16), generator=g).abs() * 4).to(torch.float8_e4m3fn)
+        ts = torch.tensor([0.013])
+    return x, codes.cuda(), scales.cuda(), ts.cuda() if ts is not None else None
+
+
+def q4_reference(x, codes, scales, ts, fmt, rotated):
+    bits = scales.cpu().view(torch.int16 if fmt == "int4" else torch.uint8).numpy()
+    bits = bits.view(np.uint16) if fmt == "int4" else bits
+    tsv = None if ts is None else ts.item()
+    xd = f64(x)
+    ref = O.q4_linear(xd, fmt, codes.cpu().numpy(), bits, tsv, rotated)
+    xa = np.abs(R.rotate_segments(xd) if rotated else xd)
+    mass = xa @ np.abs(O.q4_weight(fmt, codes.cpu().numpy(), bits, tsv)).T
+    n = x.shape[1] / 16 + 80
+    return ref, mass * (n * 2.0 ** -23 + (2.0 ** -11 if rotated else 0.0))
+
+
+Q4_SHAPES = [(1, 128, 1), (2048, 512, 1), (17, 128, 3), (300, 256, 8), (2048, 1024, 9), (129, 1152, 16), (515, 2048, 33),
+             (64, 16384, 2), (1000, 640, 64), (40, 8320, 5), (2049, 384, 70)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rotated", [True, False])
+@pytest.mark.parametrize("N,K,T", Q4_SHAPES)
+def test_q4_int4(N, K, T, rotated, dtype):
+    x, codes, scales, ts = q4_case("int4", N, K, T, dtype, N + K + T, pad=8 if N % 2 else 0)
+    y = ops.q4_linear(x, codes, scales, ts, fmt="int4", rotated=rotated)
+    ref, slack = q4_reference(x, codes, scales, ts, "int4", rotated)
+    close(y, ref, dtype, slack, 2.0 ** -11 if rotated else 0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,K,T", [(1, 16, 1), (5, 32, 2), (300, 48, 7), (77, 4112, 3), (2048, 512, 8), (130, 2064, 17), (513, 1040, 37),
+                                   (2049, 144, 65), (16, 16400, 1)])
+def test_q4_nvfp4(N, K, T, dtype):
+    x, codes, scales, ts = q4_case("nvfp4", N, K, T, dtype, N + K + T, pad=16 if T % 2 else 0)
+    y = ops.q4_linear(x, codes, scales, ts, fmt="nvfp4")
+    ref, slack = q4_reference(x, codes, scales, ts, "nvfp4", False)
+    close(y, ref, dtype, slack)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
+def test_q4_every_code_and_scale_is_exact(fmt):
+    # x = one-hot rows: y is the stored weight itself, rounded once
+    K = 128
+    codes = torch.arange(256, dtype=torch.uint8).repeat(K // 2, 1).t().contiguous().cuda()           # row b: byte b everywhere
+    if fmt == "int4":
+        vals = [2.0 ** -20, 2.0 ** -130, 1.0, 255.0, -3.0, 1.5 * 2.0 ** 100, 0.0, 0.0039]
+        scales = torch.tensor(vals, dtype=torch.float32).to(torch.bfloat16).repeat(32)[:, None].contiguous().cuda()
+        ts = None
+    else:
+        scales = torch.arange(256 * 8, dtype=torch.int64).remainder(256).to(torch.uint8)
+        scales[(scales & 0x7F) == 0x7F] = 0x38                                                       # no NaN scale
+        scales = scales.reshape(256, 8).view(torch.float8_e4m3fn).cuda()
+        ts = torch.ones(1).cuda()
+    x = torch.eye(K)[::9].contiguous().to(torch.bfloat16).cuda()
+    y = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=False)
+    ref, _ = q4_reference(x, codes, scales, ts, fmt, False)
+    np.testing.assert_array_equal(f64(y), f64(torch.from_numpy(ref).to(torch.bfloat16)))
+
+
+def test_q4_extreme_activations_stay_in_their_row():
+    # bf16 values fp16 cannot hold, tiny ones, an all-zero row, an infinity and a NaN: each token on its own
+    x, codes, scales, _ = q4_case("int4", 96, 256, 6, torch.bfloat16, 5, hot=False)
+    x = x.clone()
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    x[2] = 0
+    x[3, 7] = float("inf")
+    x[4, 200] = float("nan")
+    codes = codes.clone()
+    codes[:, 3] = (codes[:, 3] & 0x0F) | 0x30                                                        # code 3 against the infinity
+    for rotated in (False, True):
+        y = ops.q4_linear(x, codes, scales, None, fmt="int4", rotated=rotated)
+        keep = [0, 1, 2, 5]
+        ref, slack = q4_reference(x[keep], codes, scales, None, "int4", rotated)
+        close(y[keep], ref, torch.bfloat16, slack, 2.0 ** -11)
+        assert not torch.isfinite(y[3]).any() and torch.isnan(y[4]).all()
+        assert torch.all(y[2] == 0)
+        if not rotated:
+            assert torch.equal(torch.isinf(y[3]), torch.ones_like(y[3], dtype=torch.bool))
+            assert torch.equal(y[3] > 0, (scales[:, 0] > 0))
+
+
+def test_q4_writes_only_its_columns_and_repeats_bit_for_bit():
+    x, codes, scales, _ = q4_case("int4", 77, 384, 11, torch.float16, 6)
+    buf = torch.full((11, 100), 7.0, dtype=torch.float16, device="cuda")
+    ops.q4_linear(x, codes, scales, fmt="int4", y=buf[:, 3:80])
+    assert torch.all(buf[:, :3] == 7) and torch.all(buf[:, 80:] == 7)
+    assert torch.equal(buf[:, 3:80], ops.q4_linear(x, codes, scales, fmt="int4"))
+    # a token's result does not depend on its batch
+    one = torch.cat([ops.q4_linear(x[t:t + 1].contiguous(), codes, scales, fmt="int4") for t in range(11)])
+    assert torch.equal(one, buf[:, 3:80])
+
+
+def test_q4_takes_the_quantisers_output():
+    g = torch.Generator().manual_seed(3)
+    w = (torch.randn((192, 512), generator=g) * 0.05).to(torch.bfloat16).cuda()
+    x = (torch.randn((5, 512), generator=g)).to(torch.bfloat16).cuda()
+    want = f64(x) @ f64(w).T
+    for fmt, rotate in (("int4", True), ("int4", False), ("nvfp4", False)):
+        codes, scales, ts = ops.quantize_linear(w, fmt=fmt, rotate=rotate)
+        y = f64(ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=rotate))
+        # 4-bit rounding of normal weights: ~11% of each weight's rms at most, independent over K
+        assert np.linalg.norm(y - want) <= 0.15 * np.linalg.norm(want)
+
+
+# ------------------------------------------------------------------------------------------ grouped linear
+
+def counts_to_offsets(counts):
+    return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32).cuda()
+
+
+def grouped_check(counts, N, K, dtype, act, seed, gather, pad=0, tail=0, row_div=1, x_rows=None):
+    g = torch.Generator().manual_seed(seed)
+    E, P = len(counts), int(sum(counts)) + tail
+    w = (torch.randn((E, N, K), generator=g) * 0.05).to(dtype).cuda()
+    P = max(P, 1)                                    # at least one row, of no group if need be
+    n_x = x_rows or (P if not gather else max(1, P // 2))
+    x = torch.randn((n_x, K + pad), generator=g).to(dtype).cuda()[:, :K]
+    rows = torch.randint(0, n_x * row_div, (P,), generator=g).to(torch.int32).cuda() if gather else None
+    off = counts_to_offsets(counts)
+    nout = N // 2 if act == "swiglu" else N
+    buf = torch.full((P, nout + 5), 9.0, dtype=dtype, device="cuda")
+    y = ops.grouped_linear(x, w, off, rows=rows, row_div=row_div, act=act, y=buf[:, 2:2 + nout])
+    ref, live = O.grouped_linear(f64(x), f64(w), off.cpu().numpy(), None if rows is None else rows.cpu().numpy(), row_div,
+                                 act == "swiglu")
+    wa, xa = np.abs(f64(w)), np.abs(f64(x))
+    n = (K / 16 + 80) * 2.0 ** -23
+    if act == "swiglu":
+        # silu has slope below 1.1 and |silu(g)| <= |g|: the halves' errors da, db give 1.1 da |u| + |g| db, and silu
+        # itself (exponential, division) a few 2^-22
+        lin, _ = O.grouped_linear(f64(x), f64(w), off.cpu().numpy(), None if rows is None else rows.cpu().numpy(), row_div)
+        mass, _ = O.grouped_linear(xa, wa, off.cpu().numpy(), None if rows is None else rows.cpu().numpy(), row_div)
+        ga, u = np.abs(lin[:, :nout]), np.abs(lin[:, nout:])
+        slack = 1.1 * n * mass[:, :nout] * u + ga * n * mass[:, nout:] + 2.0 ** -20 * ga * u
+    else:
+        mass, _ = O.grouped_linear(xa, wa, off.cpu().numpy(), None if rows is None else rows.cpu().numpy(), row_div)
+        slack = mass * n
+    if live.any():
+        close(y, ref, dtype, slack, 2.0 ** -14, rows=live)
+    assert torch.all(buf[:, :2] == 9) and torch.all(buf[:, 2 + nout:] == 9)
+    assert torch.all(y[torch.from_numpy(~live).cuda()] == 9)
+    return y
+
+
+FEW = [[1], [0, 1, 0], [3, 0, 5, 0], [1] * 6, [0, 0, 0], [17, 1, 0, 2], [64], [0] * 200 + [2, 0, 1], [8, 9, 7, 16]]
+MANY = [[65], [100, 0, 1, 27], [0, 300, 5], [128, 129, 127, 0, 1], [40] * 9, [0, 0, 513], [1, 2, 3, 4, 5] * 20, [256, 257]]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("i", range(len(FEW)))
+def test_grouped_few_rows(i, act, dtype):
+    N, K = [(64, 64), (128, 520), (30, 8), (256, 2048), (34, 72), (200, 136), (16, 1024), (70, 256), (130, 640)][i]
+    grouped_check(FEW[i], N, K, dtype, act, i, gather=i % 2 == 1, pad=8 * (i % 3), tail=i % 2, row_div=1 + i % 3)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_grouped_many_rows(i, act, dtype):
+    N, K = [(64, 64), (128, 520), (30, 8), (256, 1024), (34, 72), (1000, 200), (16, 128), (390, 264)][i]
+    grouped_check(MANY[i], N, K, dtype, act, 50 + i, gather=i % 2 == 0, pad=8 * (i % 3), tail=3 * (i % 2), row_div=1 + i % 4)
+
+
+def test_grouped_many_experts_and_odd_widths():
+    rng = np.random.default_rng(0)
+    counts = rng.integers(0, 4, 1024)
+    grouped_check(list(counts), 19, 40, torch.bfloat16, None, 7, gather=True, row_div=6)
+    grouped_check([70, 0, 3], 1, 64, torch.float16, None, 8, gather=False)
+    grouped_check([70, 0, 3], 2, 64, torch.float16, "swiglu", 9, gather=False)
+
+
+def test_grouped_offsets_and_rows_outside_are_clamped():
+    for P in (10, 200):
+        g = torch.Generator().manual_seed(P)
+        x = torch.randn((P, 64), generator=g).to(torch.bfloat16).cuda()
+        w = (torch.randn((4, 32, 64), generator=g) * 0.1).to(torch.bfloat16).cuda()
+        off = torch.tensor([-7, 4, 4, 2, P + 1000], dtype=torch.int32).cuda()       # group 2 ends before it begins
+        rows = torch.arange(P, dtype=torch.int32).cuda()
+        rows[0], rows[P - 1] = -5, 1 << 30
+        y = torch.full((P, 32), 9.0, dtype=torch.bfloat16, device="cuda")
+        off_ok = torch.tensor([0, 4, 4, 4, P], dtype=torch.int32).cuda()
+        off_ok[3] = 4
+        ops.grouped_linear(x, w, torch.tensor([-7, 4, 4, 4, P + 1000], dtype=torch.int32).cuda(), rows=rows, y=y)
+        ref, live = O.grouped_linear(f64(x), f64(w), off_ok.cpu().numpy(), rows.cpu().numpy())
+        assert live.all()
+        close(y, ref, torch.bfloat16, 1e-4)
+        ops.grouped_linear(x, w, off, rows=rows, y=y)                               # overlapping groups: no fault
+        torch.cuda.synchronize()
+
+
+def test_grouped_nan_rows_stay_in_their_row():
+    for counts in ([5, 3], [70, 130]):
+        P = sum(counts)
+        g = torch.Generator().manual_seed(P)
+        x = torch.randn((P, 136), generator=g).to(torch.bfloat16).cuda()
+        w = (torch.randn((2, 48, 136), generator=g) * 0.1).to(torch.bfloat16).cuda()
+        off = counts_to_offsets(counts)
+        want = ops.grouped_linear(x, w, off)
+        x2 = x.clone()
+        x2[counts[0] - 1, 5] = float("nan")
+        x2[counts[0], 100] = float("inf")
+        got = ops.grouped_linear(x2, w, off)
+        keep = torch.ones(P, dtype=torch.bool, device="cuda")
+        keep[counts[0] - 1:counts[0] + 1] = False
+        assert torch.equal(got[keep], want[keep])
+        assert torch.isnan(got[counts[0] - 1]).all() and not torch.isfinite(got[counts[0]]).any()
+
+
+def test_grouped_is_deterministic():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((700, 512), generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn((8, 256, 512), generator=g) * 0.1).to(torch.bfloat16).cuda()
+    for counts in ([100, 0, 200, 1, 99, 50, 50, 200], [3, 0, 1, 1, 0, 7, 2, 0]):
+        P = sum(counts)
+        off = counts_to_offsets(counts)
+        first = ops.grouped_linear(x[:P], w, off, act="swiglu")
+        for _ in range(5):
+            assert torch.equal(ops.grouped_linear(x[:P], w, off, act="swiglu"), first)
+
+
+# ------------------------------------------------------------------------------------- permute and combine
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 6, 256), (5, 6, 256), (33, 2, 7), (64, 64, 64), (700, 6, 256), (2048, 6, 256), (4099, 1, 3),
+                                   (1500, 8, 1024), (20001, 3, 129), (1, 8, 1000)])
+@pytest.mark.parametrize("kind", ["all", "dropped", "one", "none"])
+def test_permute(T, k, E, kind):
+    g = torch.Generator().manual_seed(T + k + E)
+    ids = torch.randint(0, E, (T, k), generator=g)
+    if kind == "dropped":
+        ids = torch.randint(-3, E + 3, (T, k), generator=g)
+    elif kind == "one":
+        ids[:] = E - 1
+    elif kind == "none":
+        ids[:] = -1
+    ids = ids.to(torch.int32)
+    off, perm, inv = ops.expert_permute(ids.cuda(), E)
+    flat = ids.reshape(-1).long().numpy()
+    key = np.where((flat < 0) | (flat >= E), E, flat)
+    order = np.argsort(key, kind="stable")
+    counts = np.bincount(key, minlength=E + 1)[:E]
+    kept = int(counts.sum())
+    np.testing.assert_array_equal(off.cpu().numpy(), np.concatenate([[0], np.cumsum(counts)]))
+    want = np.where(np.arange(T * k) < kept, order, -1)
+    np.testing.assert_array_equal(perm.cpu().numpy(), want)
+    pos = np.empty(T * k, dtype=np.int64)
+    pos[order] = np.arange(T * k)
+    np.testing.assert_array_equal(inv.cpu().numpy().reshape(-1), np.where(key < E, pos, -1))
+
+
+def test_permute_of_no_tokens():
+    off, perm, inv = ops.expert_permute(torch.empty((0, 6), dtype=torch.int32, device="cuda"), 9)
+    assert torch.all(off == 0) and off.numel() == 10 and perm.numel() == 0 and inv.shape == (0, 6)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,H", [(1, 1, 1), (3, 6, 2048), (7, 2, 513), (50, 9, 64), (129, 64, 40), (300, 8, 4096), (2, 3, 8200)])
+def test_combine(T, k, H, dtype):
+    g = torch.Generator().manual_seed(T + k + H)
+    P = T * k
+    o = torch.randn((P, H + 8), generator=g).to(dtype).cuda()[:, :H]
+    inv = torch.randperm(P, generator=g).to(torch.int32).reshape(T, k)
+    inv[torch.rand((T, k), generator=g) < 0.2] = -1
+    if T > 2:
+        inv[1] = -1                                  # a token with no expert left
+        inv[2, 0] = P + 3                            # outside: skipped
+    w = torch.rand((T, k), generator=g)
+    add = torch.randn((T, H), generator=g).to(dtype).cuda()
+    o = o.clone() if H % 8 else o
+    for addend in (None, add):
+        y = ops.expert_combine(o, inv.cuda(), w.cuda(), addend=addend, scale=0.75)
+        ref = O.expert_combine(f64(o), inv.numpy(), w.double().numpy(), None if addend is None else f64(addend), 0.75)
+        mass = O.expert_combine(np.abs(f64(o)), inv.numpy(), w.double().numpy(), None if addend is None else np.abs(f64(addend)), 0.75)
+        close(y, ref, dtype, mass * (k + 4) * 2.0 ** -24)
+    inplace = add.clone()
+    assert ops.expert_combine(o, inv.cuda(), w.cuda(), addend=inplace, scale=0.75, y=inplace) is inplace
+    assert torch.equal(inplace, ops.expert_combine(o, inv.cuda(), w.cuda(), addend=add, scale=0.75))
+
+
+def test_combine_skips_dropped_rows_whatever_they_hold():
+    o = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda")
+    o[1] = float("nan")
+    inv = torch.tensor([[0, -1], [2, 3]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[2.0, float("inf")], [1.0, 0.5]], device="cuda")
+    y = ops.expert_combine(o, inv, w)
+    assert torch.all(y[0] == 2) and torch.all(y[1] == 1.5)
+
+
+# -------------------------------------------------------------------------------------------- block norm
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("res32", [True, False])
+@pytest.mark.parametrize("T,H", [(1, 1), (4, 2048), (3, 65), (17, 512), (2, 8192), (5, 8200), (2, 20000), (9, 4095), (1, 32768)])
+@pytest.mark.parametrize("mode", ["plain", "branch", "post", "gate_row", "gate_token"])
+def test_block_norm(T, H, mode, res32, dtype):
+    g = torch.Generator().manual_seed(T + H)
+    rt = torch.float32 if res32 else dtype
+    x = (torch.randn((T, H + 8), generator=g) * torch.exp2(torch.randint(-6, 6, (T, 1), generator=g).float())).to(rt).cuda()[:, :H]
+    y = torch.randn((T, H), generator=g).to(dtype).cuda() if mode != "plain" else None
+    gate = None
+    if mode.startswith("gate"):
+        gate = (2 * torch.randn((1 if mode == "gate_row" else T, H), generator=g)).to(dtype).cuda()
+    post = mode in ("post", "gate_token")
+    wt = torch.float32 if T % 2 else dtype
+    pw = (1 + 0.1 * torch.randn(H, generator=g)).to(wt).cuda() if post else None
+    qw = (1 + 0.1 * torch.randn(H, generator=g)).to(wt).cuda() if mode != "branch" else None
+    kw = dict(res_scale=0.875, branch_scale=1.5, eps=1e-5)
+    xo, z = ops.block_norm(x, y, post_norm=post, post_weight=pw, gate=gate, gate_act="sigmoid", pre_weight=qw, z_dtype=dtype, **kw)
+    rx, rz = O.block_norm(f64(x), None if y is None else f64(y), post_norm=post, post_weight=None if pw is None else f64(pw),
+                          gate=None if gate is None else f64(gate), sigmoid=True, pre_weight=None if qw is None else f64(qw), **kw)
+    # fp32 arithmetic: a dozen roundings per element on |res x| + |branch b|; a norm adds its sum's error, at most
+    # (32 + log2 terms per thread...) 64 roundings of positive terms, halved by the square root
+    parts = 0.875 * np.abs(f64(x)) + (0 if y is None else np.abs(rx - 0.875 * f64(x)))
+    sx = parts * 64 * 2.0 ** -24
+    rms = np.sqrt((rx * rx).mean(1, keepdims=True) + 1e-5)
+    qa = 1.0 if qw is None else np.abs(f64(qw))
+    sz = (sx + np.abs(rx) * 64 * 2.0 ** -24) / rms * qa + np.abs(rz) * (np.linalg.norm(sx, axis=1, keepdims=True) / np.maximum(np.linalg.norm(rx, axis=1, keepdims=True), 1e-30))
+    if rt == torch.float32:
+        assert np.all(np.abs(f64(xo) - rx) <= sx + 2.0 ** -149)
+    else:
+        close(xo, rx, rt, sx, 2.0 ** -14)
+    close(z, rz, dtype, sz, 2.0 ** -14)
+    # in place, and without one of the outputs' buffers shared
+    x2 = x.clone()
+    xo2, z2 = ops.block_norm(x2, y, post_norm=post, post_weight=pw, gate=gate, gate_act="sigmoid", pre_weight=qw, z_dtype=dtype,
+                             x_out=x2, **kw)
+    assert xo2 is x2 and torch.equal(x2, xo) and torch.equal(z2, z)
+
+
+def test_block_norm_agrees_with_the_stack_glue():
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((37, 2048), generator=g).cuda()
+    y = torch.randn((37, 2048), generator=g).to(torch.bfloat16).cuda()
+    xs, zs = x.clone(), torch.empty((37, 2048), dtype=torch.bfloat16, device="cuda")
+    B.flint_residual_rmsnorm(xs.data_ptr(), y.data_ptr(), 37, 1e-6, zs.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    xo, z = ops.block_norm(x, y, eps=1e-6)
+    assert torch.equal(xo, xs) and torch.equal(z, zs)
+
+
+def test_block_norm_rows_are_independent_and_padding_is_kept():
+    x = torch.ones((4, 100), dtype=torch.bfloat16, device="cuda")
+    x[1] = float("nan")
+    x[2] = 0
+    z = torch.full((4, 112), 5.0, dtype=torch.bfloat16, device="cuda")
+    ops.block_norm(x, z=z[:, :100])
+    assert torch.all(z[0, :100] == 1) and torch.isnan(z[1, :100]).all() and torch.all(z[2, :100] == 0) and torch.all(z[:, 100:] == 5)
+
+
+# ------------------------------------------------------------------------------------------- used together
+
+def block_inputs(T, H=256, I=128, E=16, k=4, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    bf = torch.bfloat16
+    d = dict(x=torch.randn((T, H), generator=g).cuda(), y=torch.randn((T, H), generator=g).to(bf).cuda(),
+             gu=(torch.randn((E, 2 * I, H), generator=g) / H ** 0.5).to(bf).cuda(),
+             dn=(torch.randn((E, H, I), generator=g) / I ** 0.5).to(bf).cuda(),
+             ws=(torch.randn((H, H), generator=g) / H ** 0.5).to(bf).cuda(),
+             ids=torch.stack([torch.randperm(E, generator=g)[:k].sort().values for _ in range(T)]).to(torch.int32).cuda(),
+             w=torch.softmax(torch.randn((T, k), generator=g), 1).cuda())
+    if T > 3:
+        d["ids"][3] = -1                             # a padded token: no expert
+    d["q"] = ops.quantize_linear(d["ws"], fmt="int4")
+    return d
+
+
+def block_step(d, experts, stream=None):
+    """One block: norm, 4-bit dense projection beside the routed 16-bit experts, norm after."""
+    x1, z = ops.block_norm(d["x"], d["y"], stream=stream)
+    shared = ops.q4_linear(z, *d["q"], fmt="int4", stream=stream)
+    y = experts.forward(z, d["ids"], d["w"], addend=shared, stream=stream)
+    x2, z2 = ops.block_norm(x1, y, post_norm=True, branch_scale=0.5, stream=stream)
+    return x2, z2, z, y
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 333])
+def test_a_block_of_the_operators_against_the_oracle(T):
+    d = block_inputs(T)
+    ex = ops.FlintExperts16(d["gu"], d["dn"])
+    x2, z2, z, y = block_step(d, ex)
+    x1, rz = O.block_norm(f64(d["x"]), f64(d["y"]))
+    close(z, rz, torch.bfloat16, 1e-5)
+    # each later step against the oracle on the device's own z (its rounding is checked above)
+    codes, scales, _ = d["q"]
+    shared = O.q4_linear(f64(z), "int4", codes.cpu().numpy(), scales.cpu().view(torch.int16).numpy().view(np.uint16), None, True)
+    off, perm, inv = O.expert_permute(d["ids"].cpu().numpy(), 16)
+    h, live = O.grouped_linear(f64(z), f64(d["gu"]), off, perm, 4, True)
+    o, _ = O.grouped_linear(h, f64(d["dn"]), off)
+    ry = O.expert_combine(o, inv, f64(d["w"]), shared)
+    # three bf16 roundings on the way (h, o, shared) and the output's: each at most 2^-8 of the norm it acts on
+    assert np.linalg.norm(f64(y) - ry) <= 4 * 2.0 ** -8 * np.linalg.norm(ry)
+    rx2, rz2 = O.block_norm(x1, f64(y), post_norm=True, branch_scale=0.5)
+    assert np.abs(f64(x2) - rx2).max() <= 2.0 ** -18 * np.abs(rx2).max()
+    close(z2, rz2, torch.bfloat16, 1e-5)
+
+
+def test_operators_in_a_graph_and_on_another_stream():
+    d = block_inputs(9, seed=4)
+    ex = ops.FlintExperts16(d["gu"], d["dn"])
+    want = [t.clone() for t in block_step(d, ex)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = block_step(d, ex, stream=s)
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block_step(d, ex)
+    other = block_inputs(9, seed=5)
+    fresh = [t.clone() for t in block_step({**other, "gu": d["gu"], "dn": d["dn"], "q": d["q"]}, ex)]
+    for k in ("x", "y", "ids", "w"):
+        d[k].copy_(other[k])
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, fresh):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    ds = [block_inputs(70, seed=i) for i in (6, 7)]
+    exs = [ops.FlintExperts16(d["gu"], d["dn"]) for d in ds]
+    want = [[t.clone() for t in block_step(d, e)] for d, e in zip(ds, exs)]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [block_step(d, e, stream=s) for d, e, s in zip(ds, exs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for u, v in zip(a, b):
+                assert torch.equal(u, v)
+
+
+def test_no_rows_are_no_ops():
+    e = torch.empty
+    bf = torch.bfloat16
+    assert ops.q4_linear(e((0, 128), dtype=bf, device="cuda"), e((4, 64), dtype=torch.uint8, device="cuda"),
+                         e((4, 1), dtype=bf, device="cuda")).shape == (0, 4)
+    assert ops.grouped_linear(e((0, 64), dtype=bf, device="cuda"), e((2, 8, 64), dtype=bf, device="cuda"),
+                              torch.zeros(3, dtype=torch.int32, device="cuda")).shape == (0, 8)
+    x, z = ops.block_norm(e((0, 64), device="cuda"))
+    assert x.shape == z.shape == (0, 64)

@@ -1,0 +1,122 @@
+"""Argument checks of the standalone operators on the host, before any launch. No GPU needed: the pointers
+are never dereferenced."""
+
+import ctypes
+
+import pytest
+import torch
+
+from bit_routed_expert_sigmoid_b200 import binding as B
+from bit_routed_expert_sigmoid_b200 import ops
+
+INVALID, UNSUPPORTED, OK = B.FLINT_ERR_INVALID_ARG, B.FLINT_ERR_UNSUPPORTED, B.FLINT_OK
+A, C, D, E_, F = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000        # 16-byte aligned stand-ins
+
+
+def _status(name, defaults, **kw):
+    args = dict(defaults)
+    assert set(kw) <= set(args)
+    args.update(kw)
+    return B.raw_status(name, *args.values())
+
+
+Q4 = dict(fmt=0, N=64, K=256, rotated=1, codes=A, scales=C, tscale=0, x=D, ldx=256, T=4, type=0, y=E_, ldy=64, stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(fmt=2), dict(N=0), dict(K=0), dict(K=192), dict(K=-128), dict(rotated=2), dict(fmt=1, rotated=1, tscale=F),
+    dict(fmt=1, rotated=0, tscale=0), dict(fmt=1, rotated=0, K=248, tscale=F), dict(T=-1), dict(type=2), dict(type=-1),
+    dict(ldx=255), dict(ldx=260), dict(ldx=128), dict(ldy=63), dict(codes=0), dict(codes=A + 8), dict(scales=0), dict(scales=C + 1),
+    dict(x=0), dict(x=D + 2), dict(y=0), dict(y=E_ + 1), dict(y=D), dict(tscale=F + 2)])
+def test_q4_linear_refuses(kw):
+    assert _status("flint_q4_linear", Q4, **kw) == INVALID
+
+
+def test_q4_linear_limits_and_no_op():
+    assert _status("flint_q4_linear", Q4, K=65536 + 128, ldx=65536 + 128) == UNSUPPORTED
+    assert _status("flint_q4_linear", Q4, T=0, x=0, y=0, codes=0, scales=0) == OK
+
+
+GR = dict(E=4, N=64, K=64, act=0, type=0, w=A, x=C, ldx=64, x_rows=10, row_of=0, row_div=1, offsets=D, P=10, y=E_, ldy=64,
+          stream=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(E=0), dict(N=0), dict(K=0), dict(K=60), dict(P=-1), dict(x_rows=-1), dict(row_div=0), dict(act=2), dict(type=2),
+    dict(act=1, N=63), dict(ldx=60), dict(ldx=66), dict(ldy=63), dict(act=1, ldy=31), dict(x_rows=9), dict(row_of=F, x_rows=0),
+    dict(w=0), dict(w=A + 8), dict(x=0), dict(x=C + 2), dict(y=0), dict(y=E_ + 1), dict(offsets=0), dict(offsets=D + 2),
+    dict(row_of=F + 1), dict(y=C), dict(y=A)])
+def test_grouped_linear_refuses(kw):
+    assert _status("flint_grouped_linear", GR, **kw) == INVALID
+
+
+def test_grouped_linear_limits_and_no_op():
+    for kw in (dict(E=1025), dict(K=65544, ldx=65544), dict(E=1024, N=1 << 21, ldy=1 << 21)):
+        assert _status("flint_grouped_linear", GR, **kw) == UNSUPPORTED
+    assert _status("flint_grouped_linear", GR, P=0, x_rows=0, w=0, x=0, y=0, offsets=0) == OK
+
+
+PE = dict(ids=A, T=4, top_k=2, E=8, offsets=C, perm=D, inv=E_, stream=0)
+
+
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(top_k=0), dict(E=0), dict(ids=0), dict(ids=A + 2), dict(offsets=0),
+                                dict(perm=0), dict(inv=0), dict(perm=E_), dict(perm=A), dict(inv=A + 1), dict(offsets=A)])
+def test_permute_refuses(kw):
+    assert _status("flint_expert_permute", PE, **kw) == INVALID
+
+
+def test_permute_limits():
+    for kw in (dict(top_k=65), dict(E=1025), dict(T=1 << 21, top_k=3), dict(T=2 ** 31 - 1, top_k=64)):
+        assert _status("flint_expert_permute", PE, **kw) == UNSUPPORTED
+
+
+CO = dict(o=A, ldo=64, P=8, inv=C, w=D, T=4, top_k=2, H=64, scale=ctypes.c_float(1.0), addend=E_, lda=64, type=0, y=F, ldy=64,
+          stream=0)
+
+
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(P=-1), dict(top_k=0), dict(H=0), dict(type=2), dict(ldo=63), dict(ldy=63),
+                                dict(lda=63), dict(o=0), dict(o=A + 1), dict(inv=0), dict(inv=C + 2), dict(w=0), dict(y=0),
+                                dict(y=A), dict(y=F + 1), dict(addend=E_ + 1), dict(addend=F, lda=72)])
+def test_combine_refuses(kw):
+    assert _status("flint_expert_combine", CO, **kw) == INVALID
+
+
+def test_combine_limits_and_no_op():
+    assert _status("flint_expert_combine", CO, top_k=65) == UNSUPPORTED
+    assert _status("flint_expert_combine", CO, T=0, o=0, inv=0, w=0, y=0, addend=0) == OK
+
+
+def _norm(**kw):
+    base = dict(x=A, x_out=A, y=C, gate=0, post_weight=0, pre_weight=0, z=D, ldx=64, ldxo=64, ldy=64, ldg=0, ldz=64, T=4, H=64,
+                type=0, res_type=2, w_type=2, post_norm=0, gate_act=0, res_scale=1.0, branch_scale=1.0, eps=1e-6)
+    assert set(kw) <= set(base)
+    base.update(kw)
+    return B.raw_status("flint_block_norm", ctypes.byref(B.flint_norm_args(*base.values())), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(H=0), dict(eps=0.0), dict(eps=float("nan")), dict(type=2), dict(res_type=1), dict(w_type=1), dict(post_norm=2),
+    dict(post_norm=1, y=0), dict(gate_act=2), dict(gate=E_, y=0), dict(post_weight=E_), dict(pre_weight=E_, z=0), dict(ldx=63, ldxo=63),
+    dict(ldxo=72), dict(ldy=63), dict(ldz=63), dict(gate=E_, ldg=63), dict(x=0, x_out=0), dict(x=A + 2, x_out=A + 2), dict(y=C + 1),
+    dict(z=D + 1), dict(gate=E_ + 1), dict(pre_weight=E_ + 2), dict(z=A), dict(z=C), dict(x_out=C), dict(x_out=D)])
+def test_block_norm_refuses(kw):
+    assert _norm(**kw) == INVALID
+
+
+def test_block_norm_limits_and_no_op():
+    assert B.raw_status("flint_block_norm", None, None) == INVALID
+    assert _norm(H=32776, ldx=32776, ldxo=32776, ldy=32776, ldz=32776) == UNSUPPORTED
+    assert _norm(T=0, x=0, x_out=0, y=0, z=0) == OK
+    assert _norm(x_out=0, z=0) == OK
+
+
+def test_wrappers_refuse_cpu_tensors_and_bad_shapes():
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    codes, scales = torch.zeros((4, 64), dtype=torch.uint8), torch.zeros((4, 1), dtype=torch.bfloat16)
+    for call in (lambda: ops.q4_linear(x, codes, scales),
+                 lambda: ops.grouped_linear(x, torch.zeros((1, 4, 128), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)),
+                 lambda: ops.expert_permute(torch.zeros((2, 1), dtype=torch.int32), 4),
+                 lambda: ops.expert_combine(x, torch.zeros((2, 1), dtype=torch.int32), torch.zeros((2, 1))),
+                 lambda: ops.block_norm(x)):
+        with pytest.raises(ValueError):
+            call()
