@@ -54,6 +54,7 @@ EXPORTS = (
     "flint_moe_route_noalloc", "flint_residual_rmsnorm", "flint_moe_stack_forward",
     "flint_quantize_int4_g128", "flint_quantize_nvfp4",
     "flint_q4_linear", "flint_grouped_linear", "flint_expert_permute", "flint_expert_combine", "flint_block_norm",
+    "flint_ops_error_word",
 )
 
 
@@ -118,6 +119,7 @@ def _load():
         "flint_expert_permute": (I, [V, I, I, I, V, V, V, V]),
         "flint_expert_combine": (I, [V, L, I, V, V, I, I, I, F, V, L, I, V, L, V]),
         "flint_block_norm": (I, [P(flint_norm_args), V]),
+        "flint_ops_error_word": (I, [P(ctypes.c_uint)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -266,6 +268,12 @@ def flint_expert_combine(o: int, ldo: int, P: int, inv: int, w: int, T: int, top
 
 def flint_block_norm(args: flint_norm_args, stream: int = 0) -> None:
     _check(_lib.flint_block_norm(ctypes.byref(args), stream), "flint_block_norm")
+
+
+def flint_ops_error_word() -> int:
+    out = ctypes.c_uint(0)
+    _check(_lib.flint_ops_error_word(ctypes.byref(out)), "flint_ops_error_word")
+    return int(out.value)
 
 
 def flint_moe_destroy(h: int) -> None:

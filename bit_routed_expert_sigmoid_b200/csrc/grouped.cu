@@ -1,59 +1,526 @@
-// Products grouped by expert with 16-bit weights and ragged sizes (flint_grouped_linear).
+// Products grouped by expert with 16-bit weights and ragged sizes (flint_grouped_linear):
+//   y[p] = W[e] x[r(p)] for p in [offsets[e], offsets[e+1]), or silu(gate) * up of W's two halves.
+//
+// Two kernels. grouped_mma_kernel is a persistent tcgen05 GEMM: the weights are its M side (128 rows a tile),
+// a group's rows its N side (up to NMAX a tile, padded to 16), so a group with few rows costs few columns. Both
+// operands come by TMA into the 128-byte swizzled K-major layout: the weights as boxes, the rows by gather4
+// (four rows of x by their indices per instruction), so no gathered copy of x is ever written. With few rows
+// per expert it is bound by streaming the weights once; with many, by the tensor cores.
+// grouped_few_kernel serves decode (P <= kFewRows): see there.
 #include "kernels.cuh"
 #include "ops.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
 
 namespace flint {
 
+__device__ unsigned g_ops_error;                 // timeout bits of bounded waits (flint_ops_error_word)
+
 namespace {
 
-__device__ __forceinline__ int clamp_row(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
+constexpr int kGrMaxE = 1024;
+constexpr int kGrThreads = 256;                  // 8 warps
+constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
+constexpr int kFewRows = 64;
 
-// The group that holds row p: the last e whose (clamped) offset is at or before p and whose end is behind it;
-// -1 when none does.
-__device__ __forceinline__ int group_of(const int* offsets, int E, int P, int p) {
-  for (int e = 0; e < E; ++e)
-    if (clamp_row(offsets[e], P) <= p && p < clamp_row(offsets[e + 1], P)) return e;
-  return -1;
+// First row and number of rows of group e; offsets clamped to [0, P].
+__device__ __forceinline__ int2 group_span(const int* offsets, int e, int P) {
+  const int lo = min(max(__ldg(offsets + e), 0), P), hi = min(max(__ldg(offsets + e + 1), 0), P);
+  return make_int2(lo, max(hi - lo, 0));
 }
 
-template <int TYPE>
-__global__ void __launch_bounds__(256) grouped_rows_kernel(const __grid_constant__ GroupedParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nout = p.act ? p.N / 2 : p.N;
-  __shared__ int group;
-  for (int row = blockIdx.y; row < p.P; row += gridDim.y) {
-    __syncthreads();
-    if (threadIdx.x == 0) group = group_of(p.offsets, p.E, p.P, row);
-    __syncthreads();
-    const int e = group, n = blockIdx.x * 8 + warp;
-    if (e < 0 || n >= nout) continue;
-    const int r = p.row_of ? min(max(p.row_of[row] / p.row_div, 0), p.x_rows - 1) : row;
-    const uint16_t* x = p.x + r * p.ldx;
-    const uint16_t* w = p.w + (static_cast<size_t>(e) * p.N + n) * p.K;
-    const uint16_t* u = w + static_cast<size_t>(nout) * p.K;
-    float a = 0.f, b = 0.f;
-    for (int k = lane; k < p.K; k += 32) {
-      const float xv = to_f32<TYPE>(x[k]);
-      a = fmaf(to_f32<TYPE>(w[k]), xv, a);
-      if (p.act) b = fmaf(to_f32<TYPE>(u[k]), xv, b);
-    }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, m);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, m);
-    }
-    if (lane == 0) p.y[row * p.ldy + n] = from_f32<TYPE>(p.act ? silu(a) * b : a);
+__device__ __forceinline__ int source_row(const GroupedParams& p, int row) {
+  if (!p.row_of) return row;
+  return min(max(__ldg(p.row_of + row) / p.row_div, 0), p.x_rows - 1);
+}
+
+struct GroupedMmaParams {
+  CUtensorMap tm_w, tm_x;
+  GroupedParams g;
+  int m_tiles;                                   // tiles of 128 weight rows per group
+};
+
+template <int NMAX>
+struct GrGeom {
+  static constexpr int kB = NMAX * 128;          // a stage of rows: NMAX rows x 64 K
+  static constexpr int kStage = kGrABytes + kB;
+  static constexpr int kStages = 192 * 1024 / kStage;      // 8 (64), 6 (128), 4 (256)
+};
+
+struct GrTab {
+  int start[kGrMaxE + 1];                        // first tile of group e
+  int off[kGrMaxE], cnt[kGrMaxE];
+  int wsum[kGrThreads / 32];
+  int pad;
+};
+static_assert(sizeof(GrTab) % 8 == 0, "the barriers behind it are 64-bit");
+
+struct GrBars {
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+template <int NMAX>
+constexpr int gr_smem() {
+  return GrGeom<NMAX>::kStages * GrGeom<NMAX>::kStage + static_cast<int>(sizeof(GrTab) + sizeof(GrBars)) + 1024;
+}
+static_assert(gr_smem<64>() <= 227 * 1024 && gr_smem<128>() <= 227 * 1024 && gr_smem<256>() <= 227 * 1024, "shared memory");
+
+struct GrTile {
+  int e, m, row0, n;                             // group, weight tile, first row, rows (1..NMAX)
+  bool once;                                     // the group's weights are read by no other tile
+};
+
+// Tiles of a group: weight tiles outermost, its chunks of rows (of equal size, a multiple of 16) innermost, so
+// that neighbouring CTAs share a weight tile in L2.
+template <int NMAX>
+__device__ __forceinline__ GrTile gr_tile(const GrTab& tt, int E, int t) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {                              // last group with start <= t that has tiles
+    const int mid = (lo + hi + 1) >> 1;
+    if (tt.start[mid] <= t) lo = mid;
+    else hi = mid - 1;
   }
+  const int cnt = tt.cnt[lo], nch = (cnt + NMAX - 1) / NMAX, local = t - tt.start[lo];
+  const int per = ((cnt + nch - 1) / nch + 15) & ~15;
+  GrTile r;
+  r.e = lo;
+  r.m = local / nch;
+  const int c = local - r.m * nch;
+  r.row0 = tt.off[lo] + c * per;
+  r.n = min(per, cnt - c * per);
+  r.once = nch == 1;
+  return r;
+}
+
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Waits until the copies of iterations [max(it - stages, 0), it) have landed, so that none is in flight when the
+// CTA exits. After an abort a stage may lack its other operand and never complete: each wait then ends after 1 ms,
+// far longer than a copy takes.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int it) {
+  for (int j = max(it - stages, 0); j < it; ++j) mbar_wait_bounded(&full[j % stages], (j / stages) & 1, 1000000);
+}
+
+// Warp 0: weights by TMA. Warp 2: rows by gather4. Warp 1: MMA issue. Warps 4-7: epilogue.
+template <int TYPE, int ACT, int NMAX>
+__global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
+  using G = GrGeom<NMAX>;
+  const GroupedParams& p = mp.g;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  GrTab& tt = *reinterpret_cast<GrTab*>(sm + G::kStages * G::kStage);
+  GrBars& bb = *reinterpret_cast<GrBars*>(sm + G::kStages * G::kStage + sizeof(GrTab));
+  volatile int* abort = &bb.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int steps = (p.K + 63) / 64;
+  const int nout = ACT ? p.N / 2 : p.N;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&bb.full[i], 2);
+      mbar_init(&bb.empty[i], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&bb.acc_full[a], 1);
+      mbar_init(&bb.acc_empty[a], 4);
+    }
+    mbar_init(&bb.done, 1);
+    bb.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bb.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // tile table: thread i owns the groups 4i..4i+3
+  int tiles4 = 0, first4[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = 4 * threadIdx.x + j;
+    first4[j] = tiles4;
+    if (e < p.E) {
+      const int2 s = group_span(p.offsets, e, p.P);
+      tt.off[e] = s.x;
+      tt.cnt[e] = s.y;
+      tiles4 += mp.m_tiles * ((s.y + NMAX - 1) / NMAX);
+    }
+  }
+  int incl = tiles4;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kAll, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) tt.wsum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kGrThreads / 32; ++w) {
+    if (w < warp) base += tt.wsum[w];
+    total += tt.wsum[w];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = 4 * threadIdx.x + j;
+    if (e < p.E) tt.start[e] = base + incl - tiles4 + first4[j];
+  }
+  __syncthreads();
+  const uint32_t tmem = bb.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = l2_evict_first();
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok && !*abort; t += gridDim.x) {
+        const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int slot = it % G::kStages;
+          if (it >= G::kStages && !pf_wait(&bb.empty[slot], ((it / G::kStages) - 1) & 1, abort, &g_ops_error)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = sm + slot * G::kStage;
+          mbar_arrive_expect_tx(&bb.full[slot], kGrABytes);
+          if constexpr (ACT) {
+            // 16 gate rows and the 16 up rows of the same columns alternate, so that a warp of the epilogue
+            // holds both (lanes 0-15 and 16-31)
+            const int r = tl.e * p.N + tl.m * 64;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (tl.once) {
+                tma_2d_hint(st + j * 4096, &mp.tm_w, s * 64, r + 16 * j, &bb.full[slot], pol);
+                tma_2d_hint(st + j * 4096 + 2048, &mp.tm_w, s * 64, r + nout + 16 * j, &bb.full[slot], pol);
+              } else {
+                tma_2d(st + j * 4096, &mp.tm_w, s * 64, r + 16 * j, &bb.full[slot]);
+                tma_2d(st + j * 4096 + 2048, &mp.tm_w, s * 64, r + nout + 16 * j, &bb.full[slot]);
+              }
+            }
+          } else if (tl.once) {
+            tma_2d_hint(st, &mp.tm_w, s * 64, tl.e * p.N + tl.m * 128, &bb.full[slot], pol);
+          } else {
+            tma_2d(st, &mp.tm_w, s * 64, tl.e * p.N + tl.m * 128, &bb.full[slot]);
+          }
+        }
+      }
+      drain_copies(bb.full, G::kStages, it);
+    }
+  } else if (warp == 2) {
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok && !*abort; t += gridDim.x) {
+      const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
+      const int quads = ((tl.n + 15) & ~15) / 4;             // padded rows repeat the last one: their columns are unused
+      int rows[(NMAX + 127) / 128][4];
+#pragma unroll
+      for (int h = 0; h < (NMAX + 127) / 128; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) rows[h][j] = source_row(p, tl.row0 + min(4 * (lane + 32 * h) + j, tl.n - 1));
+      for (int s = 0; s < steps; ++s, ++it) {
+        const int slot = it % G::kStages;
+        if (it >= G::kStages && !pf_wait_all(&bb.empty[slot], ((it / G::kStages) - 1) & 1, abort, &g_ops_error)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = sm + slot * G::kStage + kGrABytes;
+        if (lane == 0) mbar_arrive_expect_tx(&bb.full[slot], quads * 512);
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < (NMAX + 127) / 128; ++h)
+          if (lane + 32 * h < quads)
+            tma_gather4(st + (lane + 32 * h) * 512, &mp.tm_x, s * 64, rows[h][0], rows[h][1], rows[h][2], rows[h][3],
+                        &bb.full[slot]);
+      }
+    }
+    drain_copies(bb.full, G::kStages, it);
+  } else if (warp == 1) {
+    int it = 0, ti = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++ti) {
+      const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
+      const uint32_t idesc = idesc_m128((tl.n + 15) & ~15, TYPE == kTBf16);
+      const int as = ti & 1;
+      const uint32_t d = tmem + as * 256;
+      if (ti >= 2 && !pf_wait_all(&bb.acc_empty[as], ((ti >> 1) - 1) & 1, abort, &g_ops_error)) break;
+      tc_fence_after();
+      for (int s = 0; s < steps; ++s, ++it) {
+        const int slot = it % G::kStages;
+        if (!pf_wait_all(&bb.full[slot], (it / G::kStages) & 1, abort, &g_ops_error)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(sm + slot * G::kStage), b0 = a0 + kGrABytes;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma_ss_w(d, sdesc_sw128(a0 + ks * 32), sdesc_sw128(b0 + ks * 32), idesc, (s | ks) ? 1u : 0u);
+        tc_commit_w(&bb.empty[slot]);
+      }
+      if (ok) tc_commit_w(&bb.acc_full[as]);
+    }
+    tc_commit_w(&bb.done);
+    pf_wait_all(&bb.done, 0, abort, &g_ops_error);
+  } else if (warp >= 4) {
+    const int q = warp & 3;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    int ti = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
+      const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
+      const int as = ti & 1;
+      if (!pf_wait_all(&bb.acc_full[as], (ti >> 1) & 1, abort, &g_ops_error)) break;
+      tc_fence_after();
+      const uint32_t d = lane_base + as * 256;
+      for (int j0 = 0; j0 < tl.n; j0 += 16) {
+        uint32_t v[16];
+        tc_ld16(d + j0, v);
+        tc_wait_ld();
+        if constexpr (ACT) {
+          // lanes 0-15 hold the gate and 16-31 the up value of the same 16 outputs: of two columns the lower
+          // half takes the first and the upper half the second, with one exchange
+          const int n = tl.m * 64 + 16 * q + (lane & 15), up = lane >> 4;
+          uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0 + up) * p.ldy + n;
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float send = __uint_as_float(up ? v[c] : v[c + 1]);
+            const float got = __shfl_xor_sync(kAll, send, 16);
+            const float gate = up ? got : __uint_as_float(v[c]);
+            const float lin = up ? __uint_as_float(v[c + 1]) : got;
+            if (j0 + c + up < tl.n && n < nout) yr[c * p.ldy] = from_f32<TYPE>(silu(gate) * lin);
+          }
+        } else {
+          const int n = tl.m * 128 + 32 * q + lane;
+          uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0) * p.ldy + n;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (j0 + c < tl.n && n < nout) yr[c * p.ldy] = from_f32<TYPE>(__uint_as_float(v[c]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.acc_empty[as]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int TYPE, int ACT, int NMAX>
+cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s) {
+  GroupedMmaParams mp;
+  mp.g = p;
+  const int nout = ACT ? p.N / 2 : p.N;
+  mp.m_tiles = ACT ? (nout + 63) / 64 : (nout + 127) / 128;
+  if (!encode_16bit(&mp.tm_w, p.w, TYPE == kTBf16, static_cast<uint64_t>(p.E) * p.N, p.K, p.K, ACT ? 16 : 128) ||
+      !encode_16bit(&mp.tm_x, p.x, TYPE == kTBf16, p.x_rows, p.K, p.ldx, 1))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem_once<grouped_mma_kernel<TYPE, ACT, NMAX>>(dev, gr_smem<NMAX>());
+  if (e != cudaSuccess) return e;
+  // tiles that the rows can make at most
+  const long long chunks = p.P / NMAX + (p.E < p.P ? p.E : p.P);
+  const long long most = chunks * mp.m_tiles;
+  grouped_mma_kernel<TYPE, ACT, NMAX><<<most < sms ? static_cast<int>(most) : sms, kGrThreads, gr_smem<NMAX>(), s>>>(mp);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few rows (P <= kFewRows): bound by streaming the active groups' weights once. The weight rows of all active
+// groups are cut into units of 16 (SwiGLU: 8 gate rows and their 8 up rows) and spread evenly over one CTA per SM,
+// which a GEMM's 128-row tiles cannot do when a token has six experts. The 16 warps of a CTA split K (128 per step)
+// of a unit, or work on several units when K is short; weights go straight from global memory to the fragments of
+// mma.sync m16n8k16 (16 neighbouring K values per lane, x read with the same K order), the next step's loads in
+// flight during this one's products. Partial sums meet in shared memory and are added in warp order.
+constexpr int kFewThreads = 512;
+constexpr int kFewWarps = kFewThreads / 32;
+
+struct FewTab {
+  int n_active, pad;
+  int wsum[kFewWarps];
+  int e[kFewRows], off[kFewRows], cnt[kFewRows];
+  int src[kFewRows];                             // row of x of each row of y
+};
+
+template <int TYPE>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  const uint32_t a[4] = {a0, a1, a2, a3};
+  if constexpr (TYPE == kTBf16) mma_bf16_16816(d, a, b0, b1);
+  else mma_f16_16816(d, a, b0, b1);
+}
+
+template <int TYPE, int ACT, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __grid_constant__ GroupedParams p, int kw_n) {
+  constexpr int kUnit = ACT ? 8 : 16;            // outputs per unit
+  extern __shared__ uint8_t smem_raw[];
+  float4* red = reinterpret_cast<float4*>(smem_raw);         // [2][kFewWarps][NT][32]
+  __shared__ FewTab tab;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int nout = ACT ? p.N / 2 : p.N;
+  const int units_per = (nout + kUnit - 1) / kUnit, segs = (p.K + 127) / 128;
+
+  // active groups in ascending order: thread i looks at the groups 2i, 2i + 1
+  int2 span[2];
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 2 * threadIdx.x + j;
+    span[j] = e < p.E ? group_span(p.offsets, e, p.P) : make_int2(0, 0);
+    n += span[j].y > 0;
+  }
+  int incl = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kAll, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) tab.wsum[warp] = incl;
+  if (threadIdx.x < p.P) tab.src[threadIdx.x] = source_row(p, threadIdx.x);
+  __syncthreads();
+  int at = incl - n, total = 0;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; ++w) {
+    if (w < warp) at += tab.wsum[w];
+    total += tab.wsum[w];
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (span[j].y > 0) {
+      if (at < kFewRows) {                       // groups that overlap (bad offsets) may be more: left out
+        tab.e[at] = 2 * threadIdx.x + j;
+        tab.off[at] = span[j].x;
+        tab.cnt[at] = span[j].y;
+      }
+      ++at;
+    }
+  __syncthreads();
+  const int n_active = min(total, kFewRows);
+  const long long units = static_cast<long long>(n_active) * units_per;
+  const int u_lo = static_cast<int>(units * blockIdx.x / gridDim.x);
+  const int u_hi = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+  const int kw = warp % kw_n, ul = warp / kw_n, ul_n = kFewWarps / kw_n;
+
+  uint4 nx[8];                                   // row g: 0..3, row g + 8: 4..7; 32 neighbouring K of the step each
+  auto load = [&](int u, int s) {
+    const int ai = u / units_per, n0 = (u - ai * units_per) * kUnit + g;
+    const int n1 = ACT ? nout + n0 : n0 + 8;
+    const uint16_t* w = p.w + static_cast<size_t>(tab.e[ai]) * p.N * p.K + s * 128 + 32 * q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = s * 128 + 32 * q + 8 * i < p.K;
+      nx[i] = in && n0 < nout ? ld_stream_v4(w + static_cast<size_t>(n0) * p.K + 8 * i) : make_uint4(0, 0, 0, 0);
+      nx[4 + i] = in && (ACT ? n0 < nout : n1 < nout) ? ld_stream_v4(w + static_cast<size_t>(n1) * p.K + 8 * i)
+                                                      : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (u_lo + ul < u_hi && kw < segs) load(u_lo + ul, kw);
+  for (int b = 0, u0 = u_lo; u0 < u_hi; ++b, u0 += ul_n) {
+    const int u = u0 + ul;
+    if (u < u_hi && kw < segs) {
+      const int ai = u / units_per, cnt = min(tab.cnt[ai], 8 * NT), off = tab.off[ai];
+      float acc[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+      for (int s = kw; s < segs; s += kw_n) {
+        uint4 a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = nx[i];
+        if (s + kw_n < segs) load(u, s + kw_n);
+        else if (u + ul_n < u_hi) load(u + ul_n, kw);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (8 * t < cnt) {
+            const bool tok = 8 * t + g < cnt;
+            const uint16_t* x = p.x + (tok ? tab.src[off + 8 * t + g] * p.ldx : 0) + s * 128 + 32 * q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (tok && s * 128 + 32 * q + 8 * i < p.K) v = ld_nc_v4(x + 8 * i);
+              mma_16816<TYPE>(acc[t], a[i].x, a[4 + i].x, a[i].y, a[4 + i].y, v.x, v.y);
+              mma_16816<TYPE>(acc[t], a[i].z, a[4 + i].z, a[i].w, a[4 + i].w, v.z, v.w);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        red[(((b & 1) * kFewWarps + warp) * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    }
+    __syncthreads();                             // one per batch: the other half of red is written next
+    const float* rf = reinterpret_cast<const float*>(red + (b & 1) * kFewWarps * NT * 32);
+    const int parts = min(kw_n, segs);
+    for (int o = threadIdx.x; o < ul_n * 8 * NT * kUnit; o += kFewThreads) {
+      const int j = o % kUnit, tok = (o / kUnit) % (8 * NT), un = o / (kUnit * 8 * NT);
+      if (u0 + un >= u_hi) continue;
+      const int ai = (u0 + un) / units_per, nn = (u0 + un - ai * units_per) * kUnit + j;
+      if (tok >= tab.cnt[ai] || nn >= nout) continue;
+      const int at4 = ((un * kw_n * NT + tok / 8) * 32 + (j & 7) * 4 + (tok & 7) / 2) * 4 + (tok & 1);
+      float r0 = 0.f, r1 = 0.f;
+      for (int w = 0; w < parts; ++w) {
+        r0 += rf[at4 + w * NT * 128 + (ACT ? 0 : (j >> 3) * 2)];
+        if constexpr (ACT) r1 += rf[at4 + w * NT * 128 + 2];
+      }
+      p.y[static_cast<long long>(tab.off[ai] + tok) * p.ldy + nn] = from_f32<TYPE>(ACT ? silu(r0) * r1 : r0);
+    }
+  }
+}
+
+template <int TYPE, int ACT, int NT>
+cudaError_t launch_few(const GroupedParams& p, int dev, int sms, cudaStream_t s) {
+  constexpr int smem = 2 * kFewWarps * NT * 32 * 16;
+  cudaError_t e = allow_smem_once<grouped_few_kernel<TYPE, ACT, NT>>(dev, smem);
+  if (e != cudaSuccess) return e;
+  const int segs = (p.K + 127) / 128;
+  int kw = 1;
+  while (kw < segs && kw < kFewWarps) kw *= 2;
+  grouped_few_kernel<TYPE, ACT, NT><<<sms, kFewThreads, smem, s>>>(p, kw);
+  return cudaGetLastError();
+}
+
+template <int TYPE, int ACT>
+cudaError_t launch_type(const GroupedParams& p, cudaStream_t s) {
+  int dev, sms;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  if (p.P <= kFewRows) {
+    if (p.P <= 8) return launch_few<TYPE, ACT, 1>(p, dev, sms, s);
+    if (p.P <= 32) return launch_few<TYPE, ACT, 4>(p, dev, sms, s);
+    return launch_few<TYPE, ACT, 8>(p, dev, sms, s);
+  }
+  const long long mean = p.P / p.E;
+  if (mean <= 64) return launch_mma<TYPE, ACT, 64>(p, dev, sms, s);
+  if (mean <= 128) return launch_mma<TYPE, ACT, 128>(p, dev, sms, s);
+  return launch_mma<TYPE, ACT, 256>(p, dev, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_linear(const GroupedParams& p, cudaStream_t s) {
-  const int nout = p.act ? p.N / 2 : p.N;
-  const dim3 grid((nout + 7) / 8, p.P < 65535 ? p.P : 65535);
-  if (p.type == kTBf16) grouped_rows_kernel<kTBf16><<<grid, 256, 0, s>>>(p);
-  else grouped_rows_kernel<kTF16><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  if (p.type == kTBf16) return p.act ? launch_type<kTBf16, 1>(p, s) : launch_type<kTBf16, 0>(p, s);
+  return p.act ? launch_type<kTF16, 1>(p, s) : launch_type<kTF16, 0>(p, s);
+}
+
+// Reads and clears the current device's word (waits for the device's work).
+cudaError_t read_ops_error(unsigned* out) {
+  const unsigned zero = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(out, g_ops_error, sizeof(unsigned));
+  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_ops_error, &zero, sizeof(unsigned));
+  return e;
 }
 
 }  // namespace flint

@@ -34,6 +34,7 @@ struct GroupedParams {
   long long ldy;
 };
 cudaError_t launch_grouped_linear(const GroupedParams& p, cudaStream_t s);
+cudaError_t read_ops_error(unsigned* out);       // of the current device; waits for it, clears the word
 
 cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, int* perm, int* inv, cudaStream_t s);
 

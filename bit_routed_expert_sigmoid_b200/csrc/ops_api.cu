@@ -57,6 +57,8 @@ flint_status flint_grouped_linear(int E, int N, int K, int act, int type, const 
                                   long long ldy, void* stream) {
   if (E < 1 || N < 1 || K < 1 || K % 8 != 0 || P < 0 || x_rows < 0 || row_div < 1) return FLINT_ERR_INVALID_ARG;
   if (E > kMaxOpGroups || K > kMaxOpK || static_cast<long long>(E) * N > 0x7FFFFFFFll) return FLINT_ERR_UNSUPPORTED;
+  // tiles of 64 outputs x 64 rows are counted in 32 bits
+  if ((static_cast<long long>(N) / 64 + 1) * (P / 64 + static_cast<long long>(E)) > 0x7FFFFFFFll) return FLINT_ERR_UNSUPPORTED;
   if ((act != FLINT_ACT_NONE && act != FLINT_ACT_SWIGLU) || !is_16bit(type)) return FLINT_ERR_INVALID_ARG;
   if (act == FLINT_ACT_SWIGLU && N % 2 != 0) return FLINT_ERR_INVALID_ARG;
   if (ldx < K || ldx % 8 != 0 || ldy < (act == FLINT_ACT_SWIGLU ? N / 2 : N)) return FLINT_ERR_INVALID_ARG;
@@ -166,6 +168,11 @@ flint_status flint_block_norm(const flint_norm_args* a, void* stream) {
   p.branch_scale = a->branch_scale;
   p.eps = a->eps;
   return status_of(launch_block_norm(p, static_cast<cudaStream_t>(stream)));
+}
+
+flint_status flint_ops_error_word(unsigned* out) {
+  if (!out) return FLINT_ERR_INVALID_ARG;
+  return status_of(read_ops_error(out));
 }
 
 }  // extern "C"

@@ -1,0 +1,71 @@
+// Host helpers: TMA tensor maps, and per-device facts and one-time kernel attributes.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+namespace flint {
+
+// cuTensorMapEncodeTiled, from the driver through the runtime (no link-time driver dependency).
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 have = fn.load(std::memory_order_acquire);
+  if (!have) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      have = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+      fn.store(have, std::memory_order_release);
+    }
+  }
+  return have;
+}
+
+// 2-D map over `rows` rows of `cols` 16-bit elements, `ld` elements apart (a multiple of 8), with boxes of
+// 64 x box_rows in the 128-byte swizzle. Elements outside read as zeros.
+inline bool encode_16bit(CUtensorMap* m, const void* base, bool bf16, uint64_t rows, uint64_t cols, uint64_t ld,
+                         uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDev = 64;
+
+// SM count of the current device (looked up once per device), and the device's index.
+inline cudaError_t current_device_sms(int* dev, int* sms) {
+  static std::atomic<int> known[kMaxDev];
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  if (*dev < 0 || *dev >= kMaxDev) return cudaErrorInvalidDevice;
+  *sms = known[*dev].load(std::memory_order_relaxed);
+  if (*sms == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess) known[*dev].store(*sms, std::memory_order_relaxed);
+  }
+  return e;
+}
+
+// Allows `kernel` `bytes` of dynamic shared memory on device `dev`, once per device (setting it twice from
+// two threads is harmless).
+template <auto kernel>
+cudaError_t allow_smem_once(int dev, int bytes) {
+  static std::atomic<bool> done[kMaxDev];
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+}  // namespace flint

@@ -50,7 +50,7 @@ flint_status flint_q4_linear(int fmt, int N, int K, int rotated, const void* cod
  * a group that ends before it begins is empty. Rows of y at or behind offsets[E] are left as they were.
  * row_of int32 [P] (device) or NULL; with the permutation of flint_expert_permute or flint_moe_routing
  * (perm[p] = token * top_k + slot), row_div = top_k makes r(p) the token. r(p) outside [0, x_rows) is clamped.
- * 1 <= E <= 1024, K a multiple of 8, K <= 65536, E * N < 2^31; w and x are 16-byte aligned, ldx is a multiple
+ * 1 <= E <= 1024, K a multiple of 8, K <= 65536, E * N < 2^31, (N/64 + 1) (P/64 + E) < 2^31; w and x are 16-byte aligned, ldx is a multiple
  * of 8; y needs no alignment beyond its element's. P = 0 is a no-op. */
 flint_status flint_grouped_linear(int E, int N, int K, int act, int type, const void* w, const void* x, long long ldx,
                                   int x_rows, const int* row_of, int row_div, const int* offsets, int P, void* y,
@@ -100,6 +100,11 @@ typedef struct flint_norm_args {
 } flint_norm_args;
 
 flint_status flint_block_norm(const flint_norm_args* args, void* stream);
+
+/* Reads and clears the operators' error word of the current device: 0, or the timeout bit (4) when a bounded wait
+ * inside a kernel of flint_grouped_linear gave up since the last call (its output is then incomplete). Waits for
+ * the device. */
+flint_status flint_ops_error_word(unsigned* out);
 
 #ifdef __cplusplus
 }

@@ -499,3 +499,7 @@ def test_no_rows_are_no_ops():
                               torch.zeros(3, dtype=torch.int32, device="cuda")).shape == (0, 8)
     x, z = ops.block_norm(e((0, 64), device="cuda"))
     assert x.shape == z.shape == (0, 64)
+
+
+def test_no_wait_has_given_up():
+    assert B.flint_ops_error_word() == 0

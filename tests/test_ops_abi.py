@@ -51,7 +51,8 @@ def test_grouped_linear_refuses(kw):
 
 
 def test_grouped_linear_limits_and_no_op():
-    for kw in (dict(E=1025), dict(K=65544, ldx=65544), dict(E=1024, N=1 << 21, ldy=1 << 21)):
+    for kw in (dict(E=1025), dict(K=65544, ldx=65544), dict(E=1024, N=1 << 21, ldy=1 << 21),
+               dict(E=1, N=1 << 20, ldy=1 << 20, P=1 << 30, x_rows=1 << 30)):
         assert _status("flint_grouped_linear", GR, **kw) == UNSUPPORTED
     assert _status("flint_grouped_linear", GR, P=0, x_rows=0, w=0, x=0, y=0, offsets=0) == OK
 
@@ -108,6 +109,10 @@ def test_block_norm_limits_and_no_op():
     assert _norm(H=32776, ldx=32776, ldxo=32776, ldy=32776, ldz=32776) == UNSUPPORTED
     assert _norm(T=0, x=0, x_out=0, y=0, z=0) == OK
     assert _norm(x_out=0, z=0) == OK
+
+
+def test_error_word_needs_a_place():
+    assert B.raw_status("flint_ops_error_word", None) == INVALID
 
 
 def test_wrappers_refuse_cpu_tensors_and_bad_shapes():
