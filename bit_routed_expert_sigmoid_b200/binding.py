@@ -53,7 +53,7 @@ EXPORTS = (
     "flint_moe_status_string", "flint_moe_set_stage_events", "flint_moe_stage_count", "flint_moe_stage_name",
     "flint_moe_route_noalloc", "flint_residual_rmsnorm", "flint_moe_stack_forward",
     "flint_quantize_int4_g128", "flint_quantize_nvfp4",
-    "flint_q4_linear", "flint_grouped_linear", "flint_expert_permute", "flint_expert_combine", "flint_block_norm",
+    "flint_q4_linear", "flint_q4_linear_workspace_size", "flint_grouped_linear", "flint_expert_permute", "flint_expert_combine", "flint_block_norm",
     "flint_ops_error_word",
 )
 
@@ -114,7 +114,8 @@ def _load():
         "flint_moe_stack_forward": (I, [P(V), I, V, I, ctypes.c_float, V, V, V]),
         "flint_quantize_int4_g128": (I, [V, ctypes.c_longlong, I, I, V, V, V]),
         "flint_quantize_nvfp4": (I, [V, I, I, I, V, V, V, V]),
-        "flint_q4_linear": (I, [I, I, I, I, V, V, V, V, L, I, I, V, L, V]),
+        "flint_q4_linear_workspace_size": (S, [I, I]),
+        "flint_q4_linear": (I, [I, I, I, I, V, V, V, V, L, I, I, V, L, V, S, V]),
         "flint_grouped_linear": (I, [I, I, I, I, I, V, V, L, I, V, I, V, I, V, L, V]),
         "flint_expert_permute": (I, [V, I, I, I, V, V, V, V]),
         "flint_expert_combine": (I, [V, L, I, V, V, I, I, I, F, V, L, I, V, L, V]),
@@ -244,9 +245,14 @@ def flint_quantize_nvfp4(w: int, n_mats: int, rows: int, cols: int, codes: int, 
 
 
 def flint_q4_linear(fmt: int, N: int, K: int, rotated: int, codes: int, scales: int, tscale: int, x: int, ldx: int,
-                    T: int, type: int, y: int, ldy: int, stream: int = 0) -> None:
-    _check(_lib.flint_q4_linear(fmt, N, K, rotated, codes, scales, tscale, x, ldx, T, type, y, ldy, stream),
-           "flint_q4_linear")
+                    T: int, type: int, y: int, ldy: int, workspace: int = 0, workspace_bytes: int = 0,
+                    stream: int = 0) -> None:
+    _check(_lib.flint_q4_linear(fmt, N, K, rotated, codes, scales, tscale, x, ldx, T, type, y, ldy, workspace,
+                                workspace_bytes, stream), "flint_q4_linear")
+
+
+def flint_q4_linear_workspace_size(K: int, T: int) -> int:
+    return int(_lib.flint_q4_linear_workspace_size(K, T))
 
 
 def flint_grouped_linear(E: int, N: int, K: int, act: int, type: int, w: int, x: int, ldx: int, x_rows: int, row_of: int,

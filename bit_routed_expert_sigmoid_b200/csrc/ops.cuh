@@ -17,7 +17,9 @@ struct Q4Params {
   int T, type;
   uint16_t* y;
   long long ldy;
+  void* workspace;                               // q4_workspace_bytes(K, T), 256-byte aligned
 };
+size_t q4_workspace_bytes(int K, int T);
 cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s);
 
 struct GroupedParams {

@@ -11,6 +11,7 @@ bool opt_aligned(const void* p, uintptr_t a) { return p == nullptr || aligned_to
 bool is_16bit(int type) { return type == FLINT_T_BF16 || type == FLINT_T_F16; }
 
 constexpr int kMaxOpK = 65536;
+constexpr int kMaxQ4Tokens = 65536;              // chunks of at least 8 tokens are a grid dimension
 constexpr int kMaxOpGroups = 1024;
 constexpr int kMaxOpTopK = 64;
 constexpr long long kMaxOpPairs = 1ll << 22;
@@ -22,20 +23,27 @@ flint_status status_of(cudaError_t e) { return e == cudaSuccess ? FLINT_OK : FLI
 
 extern "C" {
 
+size_t flint_q4_linear_workspace_size(int K, int T) {
+  return K < 1 || K > kMaxOpK || T < 1 ? 0 : q4_workspace_bytes(K, T);
+}
+
 flint_status flint_q4_linear(int fmt, int N, int K, int rotated, const void* codes, const void* scales,
                              const float* tscale, const void* x, long long ldx, int T, int type, void* y, long long ldy,
-                             void* stream) {
+                             void* workspace, size_t workspace_bytes, void* stream) {
   if (fmt != FLINT_W_INT4_G128_FWHT128 && fmt != FLINT_W_NVFP4) return FLINT_ERR_INVALID_ARG;
   const bool i4 = fmt == FLINT_W_INT4_G128_FWHT128;
   if (N < 1 || K < 1 || K % (i4 ? 128 : 16) != 0 || T < 0) return FLINT_ERR_INVALID_ARG;
-  if (K > kMaxOpK) return FLINT_ERR_UNSUPPORTED;
+  if (K > kMaxOpK || T > kMaxQ4Tokens) return FLINT_ERR_UNSUPPORTED;
   if ((rotated != 0 && rotated != 1) || (rotated && !i4) || !is_16bit(type)) return FLINT_ERR_INVALID_ARG;
   if (ldx < K || ldx % 8 != 0 || ldy < N) return FLINT_ERR_INVALID_ARG;
   if (T == 0) return FLINT_OK;
   if (!aligned_to(codes, 16) || !aligned_to(scales, i4 ? 2 : 1) || !aligned_to(x, 16) || !aligned_to(y, 2) || x == y)
     return FLINT_ERR_INVALID_ARG;
   if (i4 ? !opt_aligned(tscale, 4) : !aligned_to(tscale, 4)) return FLINT_ERR_INVALID_ARG;
+  const size_t need = q4_workspace_bytes(K, T);
+  if (need && (!aligned_to(workspace, 256) || workspace_bytes < need)) return FLINT_ERR_WORKSPACE;
   Q4Params p{};
+  p.workspace = workspace;
   p.fmt = i4 ? kInt4 : kNvfp4;
   p.N = N;
   p.K = K;

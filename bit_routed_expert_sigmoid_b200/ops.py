@@ -83,8 +83,10 @@ def _q4_linear(stream, x, codes, scales, tscale, fmt, rotated, y):
         y = torch.empty((T, N), dtype=x.dtype, device=x.device)
     else:
         _need(y.shape == (T, N) and y.dtype == x.dtype, "y must be [T][N] of x's type")
+    need = B.flint_q4_linear_workspace_size(K, T)
+    ws = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
     B.flint_q4_linear(_FORMATS[fmt], N, K, 1 if rotated else 0, codes.data_ptr(), scales.data_ptr(), _ptr(tscale),
-                      x.data_ptr(), ldx, T, _TYPES[x.dtype], y.data_ptr(), _rows(y, "y"), stream)
+                      x.data_ptr(), ldx, T, _TYPES[x.dtype], y.data_ptr(), _rows(y, "y"), _ptr(ws), need, stream)
     return y
 
 

@@ -6,8 +6,8 @@
  *
  * The conventions of flint_moe.h hold: device pointers owned by the caller, work enqueued on `stream` and
  * never waited for, nothing allocated, bad arguments refused before anything is launched. Every function
- * is stateless (no handle, no workspace), so calls on different streams may overlap, and all of them can
- * be captured into CUDA graphs. The current device must be the stream's. Leading dimensions (ld*) count
+ * is stateless (no handle), so calls on different streams may overlap as long as they share no workspace,
+ * and all of them can be captured into CUDA graphs. The current device must be the stream's. Leading dimensions (ld*) count
  * elements between rows. Outputs must not overlap inputs unless a function says so. Sums run in fp32 in a
  * fixed order: the same call gives the same bits. Results are rounded once, to the output's type.
  */
@@ -33,11 +33,15 @@ extern "C" {
  *   fmt FLINT_W_NVFP4: codes u8 [N][K/2], scales E4M3 [N][K/16], K a multiple of 16; rotated = 0.
  * tscale f32 [1] (device) multiplies the sum: required for NVFP4, optional (NULL = 1) for int4.
  * x [T][K] and y [T][N] are of `type` (BF16 or F16). codes and x are 16-byte aligned and ldx is a multiple of
- * 8; y, ldy need no alignment beyond their element's. K <= 65536. Made for few tokens (T <= 64); any T runs,
- * in chunks that read the weights again. T = 0 is a no-op. */
+ * 8; y, ldy need no alignment beyond their element's. K, T <= 65536. Made for few tokens (T <= 64); larger T run
+ * in chunks that read the weights again. T = 0 is a no-op.
+ * workspace: flint_q4_linear_workspace_size(K, T) bytes of device memory (the activations as the kernel's operand),
+ * 256-byte aligned, in use until the call's work is done; may be NULL when that size is 0, as it is for the smallest
+ * calls. The size is 0 for invalid arguments too. */
+size_t flint_q4_linear_workspace_size(int K, int T);
 flint_status flint_q4_linear(int fmt, int N, int K, int rotated, const void* codes, const void* scales,
                              const float* tscale, const void* x, long long ldx, int T, int type, void* y, long long ldy,
-                             void* stream);
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 #define FLINT_ACT_NONE 0
 #define FLINT_ACT_SWIGLU 1

@@ -20,7 +20,8 @@ def _status(name, defaults, **kw):
     return B.raw_status(name, *args.values())
 
 
-Q4 = dict(fmt=0, N=64, K=256, rotated=1, codes=A, scales=C, tscale=0, x=D, ldx=256, T=4, type=0, y=E_, ldy=64, stream=0)
+Q4 = dict(fmt=0, N=64, K=256, rotated=1, codes=A, scales=C, tscale=0, x=D, ldx=256, T=4, type=0, y=E_, ldy=64,
+          workspace=0, workspace_bytes=ctypes.c_size_t(0), stream=0)
 
 
 @pytest.mark.parametrize("kw", [
@@ -34,6 +35,12 @@ def test_q4_linear_refuses(kw):
 
 def test_q4_linear_limits_and_no_op():
     assert _status("flint_q4_linear", Q4, K=65536 + 128, ldx=65536 + 128) == UNSUPPORTED
+    assert _status("flint_q4_linear", Q4, T=65537) == UNSUPPORTED
+    big = dict(T=64, K=4096, ldx=4096)                     # needs a workspace: missing, misaligned, too small
+    need = B.flint_q4_linear_workspace_size(4096, 64)
+    assert need > 0 and B.flint_q4_linear_workspace_size(256, 4) == B.flint_q4_linear_workspace_size(0, 64) == 0
+    for ws, n in ((0, need), (F + 16, need), (F, need - 1)):
+        assert _status("flint_q4_linear", Q4, **big, workspace=ws, workspace_bytes=ctypes.c_size_t(n)) == B.FLINT_ERR_WORKSPACE
     assert _status("flint_q4_linear", Q4, T=0, x=0, y=0, codes=0, scales=0) == OK
 
 
