@@ -341,8 +341,8 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
 // groups are cut into units of 16 (SwiGLU: 8 gate rows and their 8 up rows) and spread evenly over one CTA per SM,
 // which a GEMM's 128-row tiles cannot do when a token has six experts. The 16 warps of a CTA split K (128 per step)
 // of a unit, or work on several units when K is short; weights go straight from global memory to the fragments of
-// mma.sync m16n8k16 (16 neighbouring K values per lane, x read with the same K order), the next step's loads in
-// flight during this one's products. Partial sums meet in shared memory and are added in warp order.
+// mma.sync m16n8k16 (8 neighbouring K per lane and load, 64 bytes of a row per four lanes; x is read with the same K
+// order), the next step's loads in flight during this one's products. Partial sums meet in shared memory and are added in warp order.
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 
@@ -412,16 +412,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   const int u_hi = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
   const int kw = warp % kw_n, ul = warp / kw_n, ul_n = kFewWarps / kw_n;
 
-  uint4 nx[8];                                   // row g: 0..3, row g + 8: 4..7; 32 neighbouring K of the step each
+  uint4 nx[8];                                   // row g: 0..3, row g + 8: 4..7; K = 32 i + 8 q .. + 7 of the step
   auto load = [&](int u, int s) {
     const int ai = u / units_per, n0 = (u - ai * units_per) * kUnit + g;
     const int n1 = ACT ? nout + n0 : n0 + 8;
-    const uint16_t* w = p.w + static_cast<size_t>(tab.e[ai]) * p.N * p.K + s * 128 + 32 * q;
+    const uint16_t* w = p.w + static_cast<size_t>(tab.e[ai]) * p.N * p.K + s * 128 + 8 * q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = s * 128 + 32 * q + 8 * i < p.K;
-      nx[i] = in && n0 < nout ? ld_stream_v4(w + static_cast<size_t>(n0) * p.K + 8 * i) : make_uint4(0, 0, 0, 0);
-      nx[4 + i] = in && (ACT ? n0 < nout : n1 < nout) ? ld_stream_v4(w + static_cast<size_t>(n1) * p.K + 8 * i)
+      const bool in = s * 128 + 8 * q + 32 * i < p.K;
+      nx[i] = in && n0 < nout ? ld_stream_v4(w + static_cast<size_t>(n0) * p.K + 32 * i) : make_uint4(0, 0, 0, 0);
+      nx[4 + i] = in && (ACT ? n0 < nout : n1 < nout) ? ld_stream_v4(w + static_cast<size_t>(n1) * p.K + 32 * i)
                                                       : make_uint4(0, 0, 0, 0);
     }
   };
@@ -445,11 +445,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
         for (int t = 0; t < NT; ++t) {
           if (8 * t < cnt) {
             const bool tok = 8 * t + g < cnt;
-            const uint16_t* x = p.x + (tok ? tab.src[off + 8 * t + g] * p.ldx : 0) + s * 128 + 32 * q;
+            const uint16_t* x = p.x + (tok ? tab.src[off + 8 * t + g] * p.ldx : 0) + s * 128 + 8 * q;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 v = make_uint4(0, 0, 0, 0);
-              if (tok && s * 128 + 32 * q + 8 * i < p.K) v = ld_nc_v4(x + 8 * i);
+              if (tok && s * 128 + 8 * q + 32 * i < p.K) v = ld_nc_v4(x + 32 * i);
               mma_16816<TYPE>(acc[t], a[i].x, a[4 + i].x, a[i].y, a[4 + i].y, v.x, v.y);
               mma_16816<TYPE>(acc[t], a[i].z, a[4 + i].z, a[i].w, a[4 + i].w, v.z, v.w);
             }

@@ -33,7 +33,8 @@ flint_status flint_q4_linear(int fmt, int N, int K, int rotated, const void* cod
   if (fmt != FLINT_W_INT4_G128_FWHT128 && fmt != FLINT_W_NVFP4) return FLINT_ERR_INVALID_ARG;
   const bool i4 = fmt == FLINT_W_INT4_G128_FWHT128;
   if (N < 1 || K < 1 || K % (i4 ? 128 : 16) != 0 || T < 0) return FLINT_ERR_INVALID_ARG;
-  if (K > kMaxOpK || T > kMaxQ4Tokens) return FLINT_ERR_UNSUPPORTED;
+  // byte offsets inside the rows of one CTA (at least 1/1024 of them) are 32 bits wide
+  if (K > kMaxOpK || T > kMaxQ4Tokens || static_cast<long long>(N) * K > (1ll << 37)) return FLINT_ERR_UNSUPPORTED;
   if ((rotated != 0 && rotated != 1) || (rotated && !i4) || !is_16bit(type)) return FLINT_ERR_INVALID_ARG;
   if (ldx < K || ldx % 8 != 0 || ldy < N) return FLINT_ERR_INVALID_ARG;
   if (T == 0) return FLINT_OK;

@@ -93,38 +93,37 @@ struct Q4Frag {
   uint32_t s[2];
 };
 
+// n[h]: the lane's two rows, behind the row `base` points at.
 template <int FMT, bool WIDE>
-__device__ __forceinline__ void q4_load(const Q4Params& p, int n0, int n_end, int seg, Q4Frag& f) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+__device__ __forceinline__ void q4_load(const Q4Params& p, const uint8_t* codes, const uint8_t* scales, const int (&n)[2],
+                                        int seg, Q4Frag& f) {
+  const int q = threadIdx.x & 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int n = n0 + g + 8 * h;
-    f.c[h] = make_uint4(0, 0, 0, 0);
-    f.s[h] = 0;
-    if (n < n_end) {
-      const int k = seg * 128 + 32 * q;
-      const uint8_t* c = p.codes + static_cast<size_t>(n) * (p.K / 2) + k / 2;
-      if constexpr (FMT == kInt4) {
-        f.c[h] = ld_stream_v4(c);
-        f.s[h] = __ldg(reinterpret_cast<const uint16_t*>(p.scales) + static_cast<size_t>(n) * (p.K >> 7) + seg);
+    const int k = seg * 128 + 32 * q;
+    const uint8_t* c = codes + static_cast<uint32_t>(n[h]) * static_cast<uint32_t>(p.K >> 1) + (k >> 1);
+    if constexpr (FMT == kInt4) {
+      f.c[h] = ld_stream_v4(c);
+      f.s[h] = __ldg(reinterpret_cast<const uint16_t*>(scales) + static_cast<uint32_t>(n[h]) * static_cast<uint32_t>(p.K >> 7) + seg);
+    } else {
+      const uint8_t* s = scales + static_cast<uint32_t>(n[h]) * static_cast<uint32_t>(p.K >> 4) + (k >> 4);
+      f.c[h] = make_uint4(0, 0, 0, 0);
+      f.s[h] = 0;
+      if constexpr (WIDE) {                      // K a multiple of 32: codes in 16 bytes, both scales in one load
+        if (k < p.K) {
+          f.c[h] = ld_stream_v4(c);
+          f.s[h] = __ldg(reinterpret_cast<const uint16_t*>(s));
+        }
       } else {
-        const uint8_t* s = p.scales + static_cast<size_t>(n) * (p.K >> 4) + (k >> 4);
-        if constexpr (WIDE) {                    // K a multiple of 32: codes in 16 bytes, both scales in one load
-          if (k < p.K) {
-            f.c[h] = ld_stream_v4(c);
-            f.s[h] = __ldg(reinterpret_cast<const uint16_t*>(s));
-          }
-        } else {
-          if (k < p.K) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(c));
-            f.c[h].x = a.x, f.c[h].y = a.y;
-            f.s[h] = __ldg(s);
-          }
-          if (k + 16 < p.K) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(c + 8));
-            f.c[h].z = a.x, f.c[h].w = a.y;
-            f.s[h] |= static_cast<uint32_t>(__ldg(s + 1)) << 8;
-          }
+        if (k < p.K) {
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(c));
+          f.c[h].x = a.x, f.c[h].y = a.y;
+          f.s[h] = __ldg(s);
+        }
+        if (k + 16 < p.K) {
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(c + 8));
+          f.c[h].z = a.x, f.c[h].w = a.y;
+          f.s[h] |= static_cast<uint32_t>(__ldg(s + 1)) << 8;
         }
       }
     }
@@ -154,40 +153,50 @@ __device__ __forceinline__ void q4_decode(const Q4Frag& f, uint32_t (&d)[2][16])
   }
 }
 
-// NT token tiles of 8 and up to RB blocks of 16 rows at a time; kw_n warps split K, kQ4Warps / kw_n of such teams
-// take different rows.
+// NT token tiles of 8 and RB blocks of 16 rows at a time; kw_n warps split K, kQ4Warps / kw_n of such teams take
+// different rows.
 template <int FMT, int TYPE, int NT, int RB, bool WIDE, bool INLINE>
 __global__ void __launch_bounds__(kQ4Threads, 1) q4_linear_kernel(const __grid_constant__ Q4Params p, int kw_n) {
   extern __shared__ uint8_t sm[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int segs = (p.K + 127) / 128, kw = warp % kw_n, team = warp / kw_n, teams = kQ4Warps / kw_n;
   const int t0 = blockIdx.y * 8 * NT, tiles_all = INLINE ? NT : (p.T + 7) / 8;
   const int ntile = min(NT, (p.T - t0 + 7) / 8);
   float4* red = reinterpret_cast<float4*>(sm);   // [warps][RB][NT][32]
-  uint8_t* img;
-  float* fac;
+  const uint8_t* img;
   if constexpr (INLINE) img = sm + kQ4Warps * RB * NT * 512;
-  else img = static_cast<uint8_t*>(p.workspace);
-  fac = reinterpret_cast<float*>(img + static_cast<size_t>(tiles_all) * segs * kTileBytes);
+  else img = static_cast<const uint8_t*>(p.workspace);
+  const float* fac = reinterpret_cast<const float*>(img + static_cast<size_t>(tiles_all) * segs * kTileBytes);
 
-  // rows [lo, hi) of this CTA in blocks of at most 16 (equal sizes), rb blocks per team and round
+  // the CTA's rows [lo, lo + rows) in blocks of at most 16 and nearly equal size, a multiple of RB per team; lanes
+  // behind the end of a block repeat its last row (the same sectors), their results are not used
   const int lo = static_cast<int>(static_cast<long long>(p.N) * blockIdx.x / gridDim.x);
-  const int hi = static_cast<int>(static_cast<long long>(p.N) * (blockIdx.x + 1) / gridDim.x);
-  const int blocks = (hi - lo + 15) / 16, rb_n = min(RB, (blocks + teams - 1) / teams);
-  const int per = (hi - lo) / blocks, more = (hi - lo) % blocks;     // blocks of per + 1 rows, then of per
-  auto block_row = [&](int b) { return lo + b * per + min(b, more); };
+  const int rows = static_cast<int>(static_cast<long long>(p.N) * (blockIdx.x + 1) / gridDim.x) - lo;
+  const int round = teams * RB, blocks = ((rows + 15) / 16 + round - 1) / round * round;
+  const int per = rows / blocks, more = rows % blocks;              // blocks of per + 1 rows, then of per
+  auto block_row = [&](int b) { return b * per + min(b, more); };
+  const uint8_t* codes = p.codes + static_cast<size_t>(lo) * (p.K >> 1);
+  const uint8_t* scales = p.scales + static_cast<size_t>(lo) * (FMT == kInt4 ? p.K >> 6 : p.K >> 4);
 
-  Q4Frag nx[RB];
-  auto load = [&](int b0, int seg) {
+  int n[RB][2];
+  auto rows_of = [&](int b0) {
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-      if (r < rb_n && b0 + r < blocks) q4_load<FMT, WIDE>(p, block_row(b0 + r), block_row(b0 + r + 1), seg, nx[r]);
+    for (int r = 0; r < RB; ++r) {
+      const int first = block_row(b0 + r), last = max(block_row(b0 + r + 1) - 1, 0);
+      n[r][0] = min(first + g, last);
+      n[r][1] = min(first + g + 8, last);
+    }
   };
-  if (kw < segs && team * rb_n < blocks) load(team * rb_n, kw);
+  Q4Frag f[RB];
+  rows_of(team * RB);
+  if (kw < segs) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) q4_load<FMT, WIDE>(p, codes, scales, n[r], kw, f[r]);
+  }
   if constexpr (INLINE) {
     for (int i = warp; i < p.T * segs; i += kQ4Warps) {       // one token chunk: t0 is 0
       const int t = i / segs, seg = i - t * segs;
-      q4_operand<FMT, TYPE>(p, t, seg, t >> 3, NT, img, fac);
+      q4_operand<FMT, TYPE>(p, t, seg, t >> 3, NT, const_cast<uint8_t*>(img), const_cast<float*>(fac));
     }
     __syncthreads();
   } else {
@@ -195,9 +204,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_linear_kernel(const __grid_c
   }
   const float ts = p.tscale ? __ldg(p.tscale) : 1.f;
 
-  for (int b0 = 0; b0 < blocks; b0 += teams * rb_n) {
-    const int b = b0 + team * rb_n;
-    if (b < blocks && kw < segs) {
+  for (int b0 = 0; b0 < blocks; b0 += round) {
+    const int b = b0 + team * RB;
+    if (kw < segs) {
       float acc[RB][NT][4];
 #pragma unroll
       for (int r = 0; r < RB; ++r)
@@ -207,37 +216,34 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_linear_kernel(const __grid_c
           for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.f;
       for (int seg = kw; seg < segs; seg += kw_n) {
         const size_t tile0 = static_cast<size_t>(seg) * tiles_all + (INLINE ? 0 : (t0 >> 3));
-        Q4Frag cur[RB];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) cur[r] = nx[r];
-        if (seg + kw_n < segs) load(b, seg + kw_n);
-        else if (b + teams * rb_n < blocks) load(b + teams * rb_n, kw);
+        const bool same = seg + kw_n < segs;     // the next step is of the same rows
+        const int next = same ? seg + kw_n : kw;
+        if (!same && b0 + round < blocks) rows_of(b + round);
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-          if (r < rb_n && b + r < blocks) {
-            uint32_t a[2][16];
-            q4_decode<FMT>(cur[r], a);
-            const float s0 = FMT == kInt4 ? bf16_bits_to_f32(static_cast<uint16_t>(cur[r].s[0])) : 1.f;
-            const float s1 = FMT == kInt4 ? bf16_bits_to_f32(static_cast<uint16_t>(cur[r].s[1])) : 1.f;
+          uint32_t a[2][16];
+          q4_decode<FMT>(f[r], a);
+          const float s0 = FMT == kInt4 ? bf16_bits_to_f32(static_cast<uint16_t>(f[r].s[0])) : 1.f;
+          const float s1 = FMT == kInt4 ? bf16_bits_to_f32(static_cast<uint16_t>(f[r].s[1])) : 1.f;
+          if (same || b0 + round < blocks) q4_load<FMT, WIDE>(p, codes, scales, n[r], next, f[r]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if (t < ntile) {
-                const uint4* xb = reinterpret_cast<const uint4*>(img + (tile0 + t) * kTileBytes) + lane;
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int t = 0; t < NT; ++t) {
+            if (NT == 1 || t < ntile) {
+              const uint4* xb = reinterpret_cast<const uint4*>(img + (tile0 + t) * kTileBytes) + lane;
+              float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};      // two chains
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint4 x = xb[32 * i];
-                  const uint32_t m0[4] = {a[0][4 * i], a[1][4 * i], a[0][4 * i + 1], a[1][4 * i + 1]};
-                  const uint32_t m1[4] = {a[0][4 * i + 2], a[1][4 * i + 2], a[0][4 * i + 3], a[1][4 * i + 3]};
-                  mma_f16_16816(d, m0, x.x, x.y);
-                  mma_f16_16816(d, m1, x.z, x.w);
-                }
-                const float2 f = *reinterpret_cast<const float2*>(fac + (tile0 + t) * 8 + 2 * q);
-                acc[r][t][0] = fmaf(d[0] * f.x, s0, acc[r][t][0]);
-                acc[r][t][1] = fmaf(d[1] * f.y, s0, acc[r][t][1]);
-                acc[r][t][2] = fmaf(d[2] * f.x, s1, acc[r][t][2]);
-                acc[r][t][3] = fmaf(d[3] * f.y, s1, acc[r][t][3]);
+              for (int i = 0; i < 4; ++i) {
+                const uint4 x = xb[32 * i];
+                const uint32_t m0[4] = {a[0][4 * i], a[1][4 * i], a[0][4 * i + 1], a[1][4 * i + 1]};
+                const uint32_t m1[4] = {a[0][4 * i + 2], a[1][4 * i + 2], a[0][4 * i + 3], a[1][4 * i + 3]};
+                mma_f16_16816(d, m0, x.x, x.y);
+                mma_f16_16816(e, m1, x.z, x.w);
               }
+              const float2 fx = *reinterpret_cast<const float2*>(fac + (tile0 + t) * 8 + 2 * q);
+              acc[r][t][0] = fmaf(d[0] + e[0], s0 * fx.x, acc[r][t][0]);
+              acc[r][t][1] = fmaf(d[1] + e[1], s0 * fx.y, acc[r][t][1]);
+              acc[r][t][2] = fmaf(d[2] + e[2], s1 * fx.x, acc[r][t][2]);
+              acc[r][t][3] = fmaf(d[3] + e[3], s1 * fx.y, acc[r][t][3]);
             }
           }
         }
@@ -254,25 +260,21 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_linear_kernel(const __grid_c
     const int parts = min(kw_n, segs);
     for (int o = threadIdx.x; o < teams * RB * NT * 128; o += kQ4Threads) {
       const int row = o & 15, tok = (o >> 4) % (8 * NT), r = (o / (128 * NT)) % RB, tm = o / (128 * NT * RB);
-      const int blk = b0 + tm * rb_n + r;
-      if (r >= rb_n || blk >= blocks || t0 + tok >= p.T) continue;
-      const int n = block_row(blk) + row;
-      if (n >= block_row(blk + 1)) continue;
+      const int blk = b0 + tm * RB + r, m = block_row(blk) + row;
+      if (t0 + tok >= p.T || m >= block_row(blk + 1)) continue;
       const int at = (((tm * kw_n * RB + r) * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) * 4 +
                      (row >> 3) * 2 + (tok & 1);
       float v = 0.f;
       for (int w = 0; w < parts; ++w) v += rf[at + w * RB * NT * 128];
-      p.y[static_cast<long long>(t0 + tok) * p.ldy + n] = from_f32<TYPE>(v * ts);
+      p.y[static_cast<long long>(t0 + tok) * p.ldy + lo + m] = from_f32<TYPE>(v * ts);
     }
     __syncthreads();
   }
 }
 
 template <int FMT, int TYPE, int NT, int RB, bool WIDE, bool INLINE>
-cudaError_t launch_q4(const Q4Params& p, int dev, int sms, cudaStream_t s) {
+cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_t s) {
   const int segs = (p.K + 127) / 128;
-  int kw = 1;
-  while (kw < segs && kw < kQ4Warps) kw *= 2;
   const int smem = kQ4Warps * RB * NT * 512 + (INLINE ? static_cast<int>(q4_operand_bytes(NT, segs)) : 0);
   cudaError_t e = allow_smem_once<q4_linear_kernel<FMT, TYPE, NT, RB, WIDE, INLINE>>(dev, 227 * 1024);
   if (e != cudaSuccess) return e;
@@ -287,6 +289,18 @@ cudaError_t launch_q4(const Q4Params& p, int dev, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = INLINE ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, q4_linear_kernel<FMT, TYPE, NT, RB, WIDE, INLINE>, p, kw);
+}
+
+// Blocks of rows at a time: as many as a team has, so that it keeps that many 1 KB loads in flight per warp.
+template <int FMT, int TYPE, int NT, int RBMAX, bool WIDE, bool INLINE>
+cudaError_t launch_q4(const Q4Params& p, int dev, int sms, cudaStream_t s) {
+  const int segs = (p.K + 127) / 128;
+  int kw = 1;
+  while (kw < segs && kw < kQ4Warps) kw *= 2;
+  const int blocks = ((p.N + sms - 1) / sms + 15) / 16, teams = kQ4Warps / kw;
+  if (blocks <= teams) return launch_rows<FMT, TYPE, NT, 1, WIDE, INLINE>(p, dev, sms, kw, s);
+  if (RBMAX == 2 || blocks <= 2 * teams) return launch_rows<FMT, TYPE, NT, 2, WIDE, INLINE>(p, dev, sms, kw, s);
+  return launch_rows<FMT, TYPE, NT, RBMAX, WIDE, INLINE>(p, dev, sms, kw, s);
 }
 
 template <int FMT, int TYPE, bool WIDE>
