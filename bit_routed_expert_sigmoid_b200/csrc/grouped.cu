@@ -3,9 +3,10 @@
 //
 // Two kernels. grouped_mma_kernel is a persistent tcgen05 GEMM: the weights are its M side (128 rows a tile),
 // a group's rows its N side (up to NMAX a tile, padded to 16), so a group with few rows costs few columns. Both
-// operands come by TMA into the 128-byte swizzled K-major layout: the weights as boxes, the rows by gather4
-// (four rows of x by their indices per instruction), so no gathered copy of x is ever written. With few rows
-// per expert it is bound by streaming the weights once; with many, by the tensor cores.
+// operands are staged in the 128-byte swizzled K-major layout: the weights, and rows that are already in expert
+// order, as TMA boxes; rows taken through row_of by four warps with 16-byte cp.async, so no gathered copy of x is
+// ever written (TMA's gather4 measured ~70 cycles per four 128-byte rows: 4096^3 took 602 us with it). With few
+// rows per expert it is bound by streaming the weights once; with many, by the tensor cores.
 // grouped_few_kernel serves decode (P <= kFewRows): see there.
 #include "kernels.cuh"
 #include "ops.cuh"
@@ -19,7 +20,8 @@ __device__ unsigned g_ops_error;                 // timeout bits of bounded wait
 namespace {
 
 constexpr int kGrMaxE = 1024;
-constexpr int kGrThreads = 256;                  // 8 warps
+constexpr int kGrThreads = 256;                  // 8 warps, and 4 more that gather rows
+constexpr int kGrGather = 128;
 constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
 constexpr int kFewRows = 64;
 
@@ -45,6 +47,7 @@ struct GrGeom {
   static constexpr int kB = NMAX * 128;          // a stage of rows: NMAX rows x 64 K
   static constexpr int kStage = kGrABytes + kB;
   static constexpr int kStages = 192 * 1024 / kStage;      // 8 (64), 6 (128), 4 (256)
+  static constexpr int kBox = NMAX == 64 ? 16 : 32;        // rows of a TMA box of x
 };
 
 struct GrTab {
@@ -94,14 +97,17 @@ __device__ __forceinline__ GrTile gr_tile(const GrTab& tt, int E, int t) {
   return r;
 }
 
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-      : "memory");
+// 16 bytes to shared memory; zeros when !in
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Makes this thread's shared-memory writes visible to the tensor core's reads (async proxy).
+__device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Waits until the copies of iterations [max(it - stages, 0), it) have landed, so that none is in flight when the
 // CTA exits. After an abort a stage may lack its other operand and never complete: each wait then ends after 1 ms,
@@ -110,9 +116,9 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int it)
   for (int j = max(it - stages, 0); j < it; ++j) mbar_wait_bounded(&full[j % stages], (j / stages) & 1, 1000000);
 }
 
-// Warp 0: weights by TMA. Warp 2: rows by gather4. Warp 1: MMA issue. Warps 4-7: epilogue.
-template <int TYPE, int ACT, int NMAX>
-__global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
+// Warp 0: weights by TMA. Warp 1: MMA issue. Warp 2: rows by TMA, or warps 8-11 gather them. Warps 4-7: epilogue.
+template <int TYPE, int ACT, int NMAX, bool GATHER>
+__global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 1) grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
   using G = GrGeom<NMAX>;
   const GroupedParams& p = mp.g;
   extern __shared__ uint8_t smem_raw[];
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(&bb.full[i], 2);
+      mbar_init(&bb.full[i], GATHER ? 1 + kGrGather / 32 : 2);
       mbar_init(&bb.empty[i], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid
   int tiles4 = 0, first4[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int e = 4 * threadIdx.x + j;
+    const int e = 4 * threadIdx.x + j;           // warps behind the eighth own none
     first4[j] = tiles4;
     if (e < p.E) {
       const int2 s = group_span(p.offsets, e, p.P);
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid
     const int o = __shfl_up_sync(kAll, incl, d);
     if (lane >= d) incl += o;
   }
-  if (lane == 31) tt.wsum[warp] = incl;
+  if (lane == 31 && warp < kGrThreads / 32) tt.wsum[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -216,34 +222,67 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid
       }
       drain_copies(bb.full, G::kStages, it);
     }
-  } else if (warp == 2) {
+  } else if (!GATHER && warp == 2) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok && !*abort; t += gridDim.x) {
+        const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
+        const int boxes = (tl.n + G::kBox - 1) / G::kBox;    // rows behind the tile's only feed unused columns
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int slot = it % G::kStages;
+          if (it >= G::kStages && !pf_wait(&bb.empty[slot], ((it / G::kStages) - 1) & 1, abort, &g_ops_error)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = sm + slot * G::kStage + kGrABytes;
+          mbar_arrive_expect_tx(&bb.full[slot], boxes * G::kBox * 128);
+          for (int b = 0; b < boxes; ++b)
+            tma_2d(st + b * G::kBox * 128, &mp.tm_x, s * 64, tl.row0 + b * G::kBox, &bb.full[slot]);
+        }
+      }
+      drain_copies(bb.full, G::kStages, it);
+    }
+  } else if (GATHER && warp >= kGrThreads / 32) {
+    // eight lanes per row of 128 bytes; a stage is handed over kLag stages after its copies were issued
+    constexpr int kLag = G::kStages / 2, kPass = NMAX / 16;
+    const int tid = threadIdx.x - kGrThreads, c = tid & 7, r0 = tid >> 3;
+    const uint32_t dst0 = smem_u32(sm) + kGrABytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
     int it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok && !*abort; t += gridDim.x) {
+    auto hand_over = [&](int j) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.full[j % G::kStages]);
+    };
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
-      const int quads = ((tl.n + 15) & ~15) / 4;             // padded rows repeat the last one: their columns are unused
-      int rows[(NMAX + 127) / 128][4];
+      const int passes = (tl.n + 15) >> 4;                   // rows behind the last one repeat it: unused columns
+      int src[kPass];
 #pragma unroll
-      for (int h = 0; h < (NMAX + 127) / 128; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) rows[h][j] = source_row(p, tl.row0 + min(4 * (lane + 32 * h) + j, tl.n - 1));
+      for (int i = 0; i < kPass; ++i) src[i] = i < passes ? source_row(p, tl.row0 + min(r0 + 16 * i, tl.n - 1)) : 0;
       for (int s = 0; s < steps; ++s, ++it) {
         const int slot = it % G::kStages;
         if (it >= G::kStages && !pf_wait_all(&bb.empty[slot], ((it / G::kStages) - 1) & 1, abort, &g_ops_error)) {
           ok = false;
           break;
         }
-        uint8_t* st = sm + slot * G::kStage + kGrABytes;
-        if (lane == 0) mbar_arrive_expect_tx(&bb.full[slot], quads * 512);
-        __syncwarp();
+        const int k = s * 64 + 8 * c;
+        const bool in = k < p.K;
+        const uint16_t* x = p.x + (in ? k : 0);
+        const uint32_t dst = dst0 + slot * G::kStage;
 #pragma unroll
-        for (int h = 0; h < (NMAX + 127) / 128; ++h)
-          if (lane + 32 * h < quads)
-            tma_gather4(st + (lane + 32 * h) * 512, &mp.tm_x, s * 64, rows[h][0], rows[h][1], rows[h][2], rows[h][3],
-                        &bb.full[slot]);
+        for (int i = 0; i < kPass; ++i)
+          if (i < passes) cp_async16(dst + i * 2048, x + src[i] * p.ldx, in);
+        cp_async_commit();
+        if (it >= kLag) {
+          cp_async_wait<kLag>();
+          hand_over(it - kLag);
+        }
       }
     }
-    drain_copies(bb.full, G::kStages, it);
+    cp_async_wait<0>();
+    for (int j = max(it - kLag, 0); j < it; ++j) hand_over(j);
   } else if (warp == 1) {
     int it = 0, ti = 0;
     bool ok = true;
@@ -318,21 +357,22 @@ __global__ void __launch_bounds__(kGrThreads, 1) grouped_mma_kernel(const __grid
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int TYPE, int ACT, int NMAX>
+template <int TYPE, int ACT, int NMAX, bool GATHER>
 cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s) {
   GroupedMmaParams mp;
   mp.g = p;
   const int nout = ACT ? p.N / 2 : p.N;
   mp.m_tiles = ACT ? (nout + 63) / 64 : (nout + 127) / 128;
   if (!encode_16bit(&mp.tm_w, p.w, TYPE == kTBf16, static_cast<uint64_t>(p.E) * p.N, p.K, p.K, ACT ? 16 : 128) ||
-      !encode_16bit(&mp.tm_x, p.x, TYPE == kTBf16, p.x_rows, p.K, p.ldx, 1))
+      (!GATHER && !encode_16bit(&mp.tm_x, p.x, TYPE == kTBf16, p.x_rows, p.K, p.ldx, GrGeom<NMAX>::kBox)))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem_once<grouped_mma_kernel<TYPE, ACT, NMAX>>(dev, gr_smem<NMAX>());
+  cudaError_t e = allow_smem_once<grouped_mma_kernel<TYPE, ACT, NMAX, GATHER>>(dev, gr_smem<NMAX>());
   if (e != cudaSuccess) return e;
   // tiles that the rows can make at most
   const long long chunks = p.P / NMAX + (p.E < p.P ? p.E : p.P);
   const long long most = chunks * mp.m_tiles;
-  grouped_mma_kernel<TYPE, ACT, NMAX><<<most < sms ? static_cast<int>(most) : sms, kGrThreads, gr_smem<NMAX>(), s>>>(mp);
+  grouped_mma_kernel<TYPE, ACT, NMAX, GATHER><<<most < sms ? static_cast<int>(most) : sms,
+                                                GATHER ? kGrThreads + kGrGather : kGrThreads, gr_smem<NMAX>(), s>>>(mp);
   return cudaGetLastError();
 }
 
@@ -502,9 +542,10 @@ cudaError_t launch_type(const GroupedParams& p, cudaStream_t s) {
     return launch_few<TYPE, ACT, 8>(p, dev, sms, s);
   }
   const long long mean = p.P / p.E;
-  if (mean <= 64) return launch_mma<TYPE, ACT, 64>(p, dev, sms, s);
-  if (mean <= 128) return launch_mma<TYPE, ACT, 128>(p, dev, sms, s);
-  return launch_mma<TYPE, ACT, 256>(p, dev, sms, s);
+  const bool ga = p.row_of != nullptr;
+  if (mean <= 64) return ga ? launch_mma<TYPE, ACT, 64, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 64, false>(p, dev, sms, s);
+  if (mean <= 128) return ga ? launch_mma<TYPE, ACT, 128, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 128, false>(p, dev, sms, s);
+  return ga ? launch_mma<TYPE, ACT, 256, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 256, false>(p, dev, sms, s);
 }
 
 }  // namespace
