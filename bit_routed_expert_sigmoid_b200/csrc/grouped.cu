@@ -23,6 +23,7 @@ constexpr int kGrMaxE = 1024;
 constexpr int kGrThreads = 256;                  // 8 warps, and 4 more that gather rows
 constexpr int kGrGather = 128;
 constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
+constexpr int kGrSlab = 2 * 2 * 16 * 64 * 4;      // SwiGLU: two halves x (gate, up) x 16 columns x 64 rows, fp32
 constexpr int kFewRows = 64;
 
 // First row and number of rows of group e; offsets clamped to [0, P].
@@ -66,7 +67,7 @@ struct GrBars {
 
 template <int NMAX>
 constexpr int gr_smem() {
-  return GrGeom<NMAX>::kStages * GrGeom<NMAX>::kStage + static_cast<int>(sizeof(GrTab) + sizeof(GrBars)) + 1024;
+  return GrGeom<NMAX>::kStages * GrGeom<NMAX>::kStage + static_cast<int>(sizeof(GrTab) + sizeof(GrBars)) + kGrSlab + 1024;
 }
 static_assert(gr_smem<64>() <= 227 * 1024 && gr_smem<128>() <= 227 * 1024 && gr_smem<256>() <= 227 * 1024, "shared memory");
 
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
   uint8_t* sm = align1024(smem_raw);
   GrTab& tt = *reinterpret_cast<GrTab*>(sm + G::kStages * G::kStage);
   GrBars& bb = *reinterpret_cast<GrBars*>(sm + G::kStages * G::kStage + sizeof(GrTab));
+  float* slab = reinterpret_cast<float*>(sm + G::kStages * G::kStage + sizeof(GrTab) + sizeof(GrBars));
   volatile int* abort = &bb.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int steps = (p.K + 63) / 64;
@@ -199,19 +201,14 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
           }
           uint8_t* st = sm + slot * G::kStage;
           mbar_arrive_expect_tx(&bb.full[slot], kGrABytes);
-          if constexpr (ACT) {
-            // 16 gate rows and the 16 up rows of the same columns alternate, so that a warp of the epilogue
-            // holds both (lanes 0-15 and 16-31)
+          if constexpr (ACT) {                   // 64 gate rows, then the 64 up rows of the same outputs
             const int r = tl.e * p.N + tl.m * 64;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (tl.once) {
-                tma_2d_hint(st + j * 4096, &mp.tm_w, s * 64, r + 16 * j, &bb.full[slot], pol);
-                tma_2d_hint(st + j * 4096 + 2048, &mp.tm_w, s * 64, r + nout + 16 * j, &bb.full[slot], pol);
-              } else {
-                tma_2d(st + j * 4096, &mp.tm_w, s * 64, r + 16 * j, &bb.full[slot]);
-                tma_2d(st + j * 4096 + 2048, &mp.tm_w, s * 64, r + nout + 16 * j, &bb.full[slot]);
-              }
+            if (tl.once) {
+              tma_2d_hint(st, &mp.tm_w, s * 64, r, &bb.full[slot], pol);
+              tma_2d_hint(st + kGrABytes / 2, &mp.tm_w, s * 64, r + nout, &bb.full[slot], pol);
+            } else {
+              tma_2d(st, &mp.tm_w, s * 64, r, &bb.full[slot]);
+              tma_2d(st + kGrABytes / 2, &mp.tm_w, s * 64, r + nout, &bb.full[slot]);
             }
           } else if (tl.once) {
             tma_2d_hint(st, &mp.tm_w, s * 64, tl.e * p.N + tl.m * 128, &bb.full[slot], pol);
@@ -310,34 +307,44 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
     }
     tc_commit_w(&bb.done);
     pf_wait_all(&bb.done, 0, abort, &g_ops_error);
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     const int q = warp & 3;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    int ti = 0;
+    int ti = 0, half = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
       const int as = ti & 1;
-      if (!pf_wait_all(&bb.acc_full[as], (ti >> 1) & 1, abort, &g_ops_error)) break;
+      const bool ok = pf_wait_all(&bb.acc_full[as], (ti >> 1) & 1, abort, &g_ops_error);
+      if (named_bar_or(1, 128, !ok)) break;      // the four warps give up together: they meet at barriers below
       tc_fence_after();
       const uint32_t d = lane_base + as * 256;
-      for (int j0 = 0; j0 < tl.n; j0 += 16) {
-        uint32_t v[16];
-        tc_ld16(d + j0, v);
-        tc_wait_ld();
-        if constexpr (ACT) {
-          // lanes 0-15 hold the gate and 16-31 the up value of the same 16 outputs: of two columns the lower
-          // half takes the first and the upper half the second, with one exchange
-          const int n = tl.m * 64 + 16 * q + (lane & 15), up = lane >> 4;
-          uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0 + up) * p.ldy + n;
+      if constexpr (ACT) {
+        // warps 0, 1 hold the gate and 2, 3 the up values of the same 64 outputs: of 32 columns, each side hands 16
+        // to the other through shared memory and finishes the other 16
+        const int r = 32 * (q & 1) + lane, n = tl.m * 64 + r, up = q >> 1;
+        for (int j0 = 0; j0 < tl.n; j0 += 32, half ^= 1) {
+          uint32_t own[16], give[16];
+          tc_ld16(d + j0 + 16 * up, own);
+          tc_ld16(d + j0 + 16 * (up ^ 1), give);
+          tc_wait_ld();
+          float* to = slab + ((half * 2 + up) * 16) * 64 + r;
+          const float* from = slab + ((half * 2 + (up ^ 1)) * 16) * 64 + r;
 #pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float send = __uint_as_float(up ? v[c] : v[c + 1]);
-            const float got = __shfl_xor_sync(kAll, send, 16);
-            const float gate = up ? got : __uint_as_float(v[c]);
-            const float lin = up ? __uint_as_float(v[c + 1]) : got;
-            if (j0 + c + up < tl.n && n < nout) yr[c * p.ldy] = from_f32<TYPE>(silu(gate) * lin);
+          for (int c = 0; c < 16; ++c) to[c * 64] = __uint_as_float(give[c]);
+          named_bar_sync(1, 128);                // the next round writes the slab's other half
+          uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0 + 16 * up) * p.ldy + n;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float o = from[c * 64], v = __uint_as_float(own[c]);
+            const float h = up ? silu(o) * v : silu(v) * o;
+            if (j0 + 16 * up + c < tl.n && n < nout) yr[c * p.ldy] = from_f32<TYPE>(h);
           }
-        } else {
+        }
+      } else {
+        for (int j0 = 0; j0 < tl.n; j0 += 16) {
+          uint32_t v[16];
+          tc_ld16(d + j0, v);
+          tc_wait_ld();
           const int n = tl.m * 128 + 32 * q + lane;
           uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0) * p.ldy + n;
 #pragma unroll
@@ -363,7 +370,7 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
   mp.g = p;
   const int nout = ACT ? p.N / 2 : p.N;
   mp.m_tiles = ACT ? (nout + 63) / 64 : (nout + 127) / 128;
-  if (!encode_16bit(&mp.tm_w, p.w, TYPE == kTBf16, static_cast<uint64_t>(p.E) * p.N, p.K, p.K, ACT ? 16 : 128) ||
+  if (!encode_16bit(&mp.tm_w, p.w, TYPE == kTBf16, static_cast<uint64_t>(p.E) * p.N, p.K, p.K, ACT ? 64 : 128) ||
       (!GATHER && !encode_16bit(&mp.tm_x, p.x, TYPE == kTBf16, p.x_rows, p.K, p.ldx, GrGeom<NMAX>::kBox)))
     return cudaErrorInvalidValue;
   cudaError_t e = allow_smem_once<grouped_mma_kernel<TYPE, ACT, NMAX, GATHER>>(dev, gr_smem<NMAX>());
