@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libflint_moe.so")
 
@@ -119,7 +120,7 @@ def _load():
         "flint_grouped_linear": (I, [I, I, I, I, I, V, V, L, I, V, I, V, I, V, L, V]),
         "flint_expert_permute": (I, [V, I, I, I, V, V, V, V]),
         "flint_expert_combine": (I, [V, L, I, V, V, I, I, I, F, V, L, I, V, L, V]),
-        "flint_block_norm": (I, [P(flint_norm_args), V]),
+        "flint_block_norm": (I, [V, V]),
         "flint_ops_error_word": (I, [P(ctypes.c_uint)]),
     }
     for name, (res, args) in sig.items():
@@ -272,8 +273,13 @@ def flint_expert_combine(o: int, ldo: int, P: int, inv: int, w: int, T: int, top
            "flint_expert_combine")
 
 
-def flint_block_norm(args: flint_norm_args, stream: int = 0) -> None:
-    _check(_lib.flint_block_norm(ctypes.byref(args), stream), "flint_block_norm")
+# the bytes of a flint_norm_args from its fields in order (several times cheaper than building the Structure)
+pack_norm_args = struct.Struct("@7Q5q7i3f").pack
+
+
+def flint_block_norm(args, stream: int = 0) -> None:
+    """args: a flint_norm_args or its bytes (pack_norm_args)."""
+    _check(_lib.flint_block_norm(args if isinstance(args, bytes) else ctypes.byref(args), stream), "flint_block_norm")
 
 
 def flint_ops_error_word() -> int:

@@ -4,6 +4,9 @@ As in `layer`, PyTorch supplies device memory and streams only; every step runs 
 kernels. Shapes, types and strides are checked here (ValueError) or by the C entry points (FlintError).
 Outputs that are not given are allocated. Work goes to `stream` (default: the current stream of the
 inputs' device); an input written on another stream must have been ordered before it by the caller.
+
+The smallest calls take a few microseconds on the device, so the common path (tensors of the current
+device, its current stream) goes straight to the entry point.
 """
 
 from __future__ import annotations
@@ -17,41 +20,52 @@ _FORMATS = {"int4": B.FLINT_W_INT4_G128_FWHT128, "nvfp4": B.FLINT_W_NVFP4}
 _ACTS = {None: B.FLINT_ACT_NONE, "none": B.FLINT_ACT_NONE, "swiglu": B.FLINT_ACT_SWIGLU}
 _GATES = {None: B.FLINT_GATE_NONE, "none": B.FLINT_GATE_NONE, "sigmoid": B.FLINT_GATE_SIGMOID}
 
+_current_device = torch.cuda.current_device
+
+
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without building a Stream object around it, where torch offers that
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _elsewhere(device, stream) -> bool:
+    """Whether a call must switch device or stream first."""
+    return stream is not None or device.type != "cuda" or device.index != _current_device()
+
+
+def _switched(fn, device, stream, *args, **kw):
+    """fn with `stream` current (its device too), or with the tensors' device current."""
+    if device.type != "cuda":
+        raise ValueError("the operators run on CUDA tensors only")
+    if stream is None:
+        with torch.cuda.device(device):
+            return fn(*args, **kw)
+    _need(stream.device == device, "the stream belongs to another device than the tensors")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
 
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _check_cuda(device, **tensors) -> None:
-    for name, t in tensors.items():
+def _together(device, *tensors) -> None:
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+            raise ValueError(f"a tensor is on {t.device}, not on {device}")
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a matrix whose columns are neighbours."""
+    if t.is_contiguous() and t.dim() == 2:
+        return t.shape[1]
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a matrix with contiguous rows")
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _on_stream(fn, device, stream, *args, **kw):
-    """Runs fn with `stream` current (its device too), or with the tensors' device current."""
-    if device.type != "cuda":
-        raise ValueError("the operators run on CUDA tensors only")
-    if stream is not None:
-        _need(stream.device == device, "the stream belongs to another device than the tensors")
-        with torch.cuda.stream(stream):
-            return fn(stream.cuda_stream, *args, **kw)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return fn(torch.cuda.current_stream(device).cuda_stream, *args, **kw)
-    return fn(torch.cuda.current_stream(device).cuda_stream, *args, **kw)
-
-
-def _ptr(t) -> int:
-    return 0 if t is None else t.data_ptr()
 
 
 def q4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tscale: torch.Tensor | None = None, *,
@@ -60,55 +74,54 @@ def q4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tscale
 
     codes u8 [N][K/2]; scales bf16 [N][K/128] ("int4") or float8_e4m3fn / uint8 [N][K/16] ("nvfp4", which is
     never rotated); tscale f32 [1]. x may be rows of a wider matrix (row stride a multiple of 8 elements)."""
-    return _on_stream(_q4_linear, x.device, stream, x, codes, scales, tscale, fmt, rotated, y)
-
-
-def _q4_linear(stream, x, codes, scales, tscale, fmt, rotated, y):
-    if fmt not in _FORMATS or x.dtype not in _TYPES:
+    dev = x.device
+    if _elsewhere(dev, stream):
+        return _switched(q4_linear, dev, stream, x, codes, scales, tscale, fmt=fmt, rotated=rotated, y=y)
+    f, dt = _FORMATS.get(fmt), _TYPES.get(x.dtype)
+    if f is None or dt is None:
         raise ValueError(f"format {fmt!r} with {x.dtype} activations")
     ldx = _rows(x, "x")
     T, K = x.shape
     N = codes.shape[0]
-    _need(codes.dtype == torch.uint8 and codes.shape == (N, K // 2) and K % 2 == 0 and codes.is_contiguous(),
-          "codes must be contiguous u8 [N][K/2]")
-    if fmt == "int4":
-        _need(scales.dtype in (torch.bfloat16, torch.int16) and scales.shape == (N, K // 128), "scales must be bf16 [N][K/128]")
-    else:
-        rotated = False
-        _need(scales.element_size() == 1 and scales.shape == (N, K // 16), "scales must be E4M3 [N][K/16]")
-    _need(scales.is_contiguous(), "scales must be contiguous")
-    _need(tscale is None or (tscale.dtype == torch.float32 and tscale.numel() == 1), "tscale must be f32 [1]")
-    _check_cuda(x.device, codes=codes, scales=scales, tscale=tscale, y=y)
+    group = 128 if fmt == "int4" else 16
+    if codes.dtype != torch.uint8 or codes.shape != (N, K // 2) or K % 2 or not codes.is_contiguous():
+        raise ValueError("codes must be contiguous u8 [N][K/2]")
+    if scales.shape != (N, K // group) or scales.element_size() != (2 if group == 128 else 1) or not scales.is_contiguous():
+        raise ValueError("scales must be contiguous bf16 [N][K/128] (int4) or E4M3 [N][K/16] (nvfp4)")
+    if tscale is not None and (tscale.dtype != torch.float32 or tscale.numel() != 1):
+        raise ValueError("tscale must be f32 [1]")
+    _together(dev, codes, scales, tscale, y)
     if y is None:
-        y = torch.empty((T, N), dtype=x.dtype, device=x.device)
+        y, ldy = x.new_empty((T, N)), N
     else:
         _need(y.shape == (T, N) and y.dtype == x.dtype, "y must be [T][N] of x's type")
+        ldy = _rows(y, "y")
     need = B.flint_q4_linear_workspace_size(K, T)
-    ws = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
-    B.flint_q4_linear(_FORMATS[fmt], N, K, 1 if rotated else 0, codes.data_ptr(), scales.data_ptr(), _ptr(tscale),
-                      x.data_ptr(), ldx, T, _TYPES[x.dtype], y.data_ptr(), _rows(y, "y"), _ptr(ws), need, stream)
+    ws = x.new_empty((need,), dtype=torch.uint8) if need else None
+    B.flint_q4_linear(f, N, K, 1 if rotated and group == 128 else 0, codes.data_ptr(), scales.data_ptr(),
+                      0 if tscale is None else tscale.data_ptr(), x.data_ptr(), ldx, T, dt, y.data_ptr(), ldy,
+                      ws.data_ptr() if need else 0, need, _stream_of(dev.index))
     return y
 
 
 def quantize_linear(w: torch.Tensor, *, fmt: str = "int4", rotate: bool = True, stream=None) -> tuple:
     """bf16 w [N][K] -> (codes, scales, tscale) for q4_linear, by the library's quantisers (flint_quant.h);
     tscale is None for int4."""
+    if _elsewhere(w.device, stream):
+        return _switched(quantize_linear, w.device, stream, w, fmt=fmt, rotate=rotate)
     _need(fmt in _FORMATS and w.dtype == torch.bfloat16 and w.dim() == 2 and w.is_contiguous(),
           "w must be contiguous bf16 [N][K]")
-    _need(w.shape[0] > 0 and w.shape[1] % (128 if fmt == "int4" else 16) == 0, "K must be a multiple of the scale group")
-    return _on_stream(_quantize_linear, w.device, stream, w, fmt, rotate)
-
-
-def _quantize_linear(stream, w, fmt, rotate):
     N, K = w.shape
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+    _need(N > 0 and K % (128 if fmt == "int4" else 16) == 0, "K must be a multiple of the scale group")
+    s = _stream_of(w.device.index)
+    codes = w.new_empty((N, K // 2), dtype=torch.uint8)
     if fmt == "int4":
-        scales = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w.device)
-        B.flint_quantize_int4_g128(w.data_ptr(), N, K, rotate, codes.data_ptr(), scales.data_ptr(), stream)
+        scales = w.new_empty((N, K // 128))
+        B.flint_quantize_int4_g128(w.data_ptr(), N, K, rotate, codes.data_ptr(), scales.data_ptr(), s)
         return codes, scales, None
-    scales = torch.empty((N, K // 16), dtype=torch.float8_e4m3fn, device=w.device)
-    tscale = torch.empty((1,), dtype=torch.float32, device=w.device)
-    B.flint_quantize_nvfp4(w.data_ptr(), 1, N, K, codes.data_ptr(), scales.data_ptr(), tscale.data_ptr(), stream)
+    scales = w.new_empty((N, K // 16), dtype=torch.float8_e4m3fn)
+    tscale = w.new_empty((1,), dtype=torch.float32)
+    B.flint_quantize_nvfp4(w.data_ptr(), 1, N, K, codes.data_ptr(), scales.data_ptr(), tscale.data_ptr(), s)
     return codes, scales, tscale
 
 
@@ -119,44 +132,49 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, r
 
     x [x_rows][K], w [E][N][K] contiguous, offsets int32 [E+1], rows int32 [P]. Rows of y at or behind
     offsets[E] are left as they were (uninitialised when y is allocated here)."""
-    return _on_stream(_grouped_linear, x.device, stream, x, w, offsets, rows, row_div, act, y)
-
-
-def _grouped_linear(stream, x, w, offsets, rows, row_div, act, y):
-    if act not in _ACTS or x.dtype not in _TYPES or w.dtype != x.dtype:
+    dev = x.device
+    if _elsewhere(dev, stream):
+        return _switched(grouped_linear, dev, stream, x, w, offsets, rows=rows, row_div=row_div, act=act, y=y)
+    a, dt = _ACTS.get(act), _TYPES.get(x.dtype)
+    if a is None or dt is None or w.dtype != x.dtype:
         raise ValueError(f"act {act!r} with {x.dtype} activations and {w.dtype} weights")
     ldx = _rows(x, "x")
-    _need(w.dim() == 3 and w.is_contiguous() and w.shape[2] == x.shape[1], "w must be contiguous [E][N][K]")
+    if w.dim() != 3 or not w.is_contiguous() or w.shape[2] != x.shape[1]:
+        raise ValueError("w must be contiguous [E][N][K]")
     E, N, K = w.shape
-    _need(offsets.dtype == torch.int32 and offsets.shape == (E + 1,) and offsets.is_contiguous(),
-          "offsets must be int32 [E+1]")
-    _need(rows is None or (rows.dtype == torch.int32 and rows.dim() == 1 and rows.is_contiguous()), "rows must be int32 [P]")
-    _check_cuda(x.device, w=w, offsets=offsets, rows=rows, y=y)
-    P = x.shape[0] if rows is None else rows.shape[0]
-    a = _ACTS[act]
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous int32 [E+1]")
+    if rows is None:
+        P = x.shape[0]
+    else:
+        if rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous():
+            raise ValueError("rows must be contiguous int32 [P]")
+        P = rows.shape[0]
+    _together(dev, w, offsets, rows, y)
     nout = N // 2 if a else N
     if y is None:
-        y = torch.empty((P, nout), dtype=x.dtype, device=x.device)
+        y, ldy = x.new_empty((P, nout)), nout
     else:
         _need(y.shape == (P, nout) and y.dtype == x.dtype, "y must be [P][N], [P][N/2] with swiglu, of x's type")
-    B.flint_grouped_linear(E, N, K, a, _TYPES[x.dtype], w.data_ptr(), x.data_ptr(), ldx, x.shape[0], _ptr(rows), row_div,
-                           offsets.data_ptr(), P, y.data_ptr(), _rows(y, "y"), stream)
+        ldy = _rows(y, "y")
+    B.flint_grouped_linear(E, N, K, a, dt, w.data_ptr(), x.data_ptr(), ldx, x.shape[0],
+                           0 if rows is None else rows.data_ptr(), row_div, offsets.data_ptr(), P, y.data_ptr(), ldy,
+                           _stream_of(dev.index))
     return y
 
 
 def expert_permute(ids: torch.Tensor, n_experts: int, *, stream=None) -> tuple:
     """ids int32 [T][top_k] -> (offsets [E+1], perm [T*top_k], inv [T][top_k]), all int32: the expert-major
     order of the (token, slot) pairs. Ids outside [0, E) are dropped (flint_expert_permute)."""
-    return _on_stream(_expert_permute, ids.device, stream, ids, n_experts)
-
-
-def _expert_permute(stream, ids, E):
-    _need(ids.dtype == torch.int32 and ids.dim() == 2 and ids.is_contiguous(), "ids must be contiguous int32 [T][top_k]")
+    dev = ids.device
+    if _elsewhere(dev, stream):
+        return _switched(expert_permute, dev, stream, ids, n_experts)
+    if ids.dtype != torch.int32 or ids.dim() != 2 or not ids.is_contiguous() or n_experts < 1:
+        raise ValueError("ids must be contiguous int32 [T][top_k], and at least one expert")
     T, K = ids.shape
-    offsets = torch.empty((max(int(E), 0) + 1,), dtype=torch.int32, device=ids.device)
-    perm = torch.empty((T * K,), dtype=torch.int32, device=ids.device)
-    inv = torch.empty((T, K), dtype=torch.int32, device=ids.device)
-    B.flint_expert_permute(ids.data_ptr(), T, K, int(E), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), stream)
+    offsets, perm, inv = ids.new_empty((n_experts + 1,)), ids.new_empty((T * K,)), ids.new_empty((T, K))
+    B.flint_expert_permute(ids.data_ptr(), T, K, n_experts, offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(),
+                           _stream_of(dev.index))
     return offsets, perm, inv
 
 
@@ -164,26 +182,31 @@ def expert_combine(o: torch.Tensor, inv: torch.Tensor, w: torch.Tensor, *, adden
                    scale: float = 1.0, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[t] = scale * sum_k w[t][k] o[inv[t][k]] + addend[t]; slots with inv < 0 are skipped
     (flint_expert_combine). o [P][H], inv int32 and w f32 [T][top_k], addend [T][H] (may be y)."""
-    return _on_stream(_expert_combine, o.device, stream, o, inv, w, addend, scale, y)
-
-
-def _expert_combine(stream, o, inv, w, addend, scale, y):
-    if o.dtype not in _TYPES:
+    dev = o.device
+    if _elsewhere(dev, stream):
+        return _switched(expert_combine, dev, stream, o, inv, w, addend=addend, scale=scale, y=y)
+    dt = _TYPES.get(o.dtype)
+    if dt is None:
         raise ValueError(f"expert rows of {o.dtype}")
     ldo = _rows(o, "o")
-    _need(inv.dtype == torch.int32 and inv.dim() == 2 and inv.is_contiguous(), "inv must be contiguous int32 [T][top_k]")
-    _need(w.dtype == torch.float32 and w.shape == inv.shape and w.is_contiguous(), "w must be contiguous f32 [T][top_k]")
+    if inv.dtype != torch.int32 or inv.dim() != 2 or not inv.is_contiguous():
+        raise ValueError("inv must be contiguous int32 [T][top_k]")
+    if w.dtype != torch.float32 or w.shape != inv.shape or not w.is_contiguous():
+        raise ValueError("w must be contiguous f32 [T][top_k]")
     T, K = inv.shape
     P, H = o.shape
-    _need(addend is None or (addend.shape == (T, H) and addend.dtype == o.dtype), "addend must be [T][H] of o's type")
-    _check_cuda(o.device, inv=inv, w=w, addend=addend, y=y)
+    add = lda = 0
+    if addend is not None:
+        _need(addend.shape == (T, H) and addend.dtype == o.dtype, "addend must be [T][H] of o's type")
+        add, lda = addend.data_ptr(), _rows(addend, "addend")
+    _together(dev, inv, w, addend, y)
     if y is None:
-        y = torch.empty((T, H), dtype=o.dtype, device=o.device)
+        y, ldy = o.new_empty((T, H)), H
     else:
         _need(y.shape == (T, H) and y.dtype == o.dtype, "y must be [T][H] of o's type")
-    B.flint_expert_combine(o.data_ptr(), ldo, P, inv.data_ptr(), w.data_ptr(), T, K, H, scale, _ptr(addend),
-                           0 if addend is None else _rows(addend, "addend"), _TYPES[o.dtype], y.data_ptr(),
-                           _rows(y, "y"), stream)
+        ldy = _rows(y, "y")
+    B.flint_expert_combine(o.data_ptr(), ldo, P, inv.data_ptr(), w.data_ptr(), T, K, H, scale, add, lda, dt, y.data_ptr(),
+                           ldy, _stream_of(dev.index))
     return y
 
 
@@ -197,44 +220,53 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: boo
 
     x [T][H] fp32 or the branch's type; y [T][H]; gate [T][H], [1][H] or [H]; weights [H], fp32 or the branch's
     type (both the same). x_out may be x (in place). z has the branch's type (z_dtype without a branch)."""
-    return _on_stream(_block_norm, x.device, stream, x, y, post_norm, post_weight, gate, gate_act, res_scale,
-                      branch_scale, pre_weight, eps, x_out, z, z_dtype)
-
-
-def _block_norm(stream, x, y, post_norm, post_weight, gate, gate_act, res_scale, branch_scale, pre_weight, eps, x_out, z,
-                z_dtype):
+    dev = x.device
+    if _elsewhere(dev, stream):
+        return _switched(block_norm, dev, stream, x, y, post_norm=post_norm, post_weight=post_weight, gate=gate,
+                         gate_act=gate_act, res_scale=res_scale, branch_scale=branch_scale, pre_weight=pre_weight, eps=eps,
+                         x_out=x_out, z=z, z_dtype=z_dtype)
     ldx = _rows(x, "x")
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
+    xt = x.dtype
     dt = y.dtype if y is not None else z.dtype if z is not None else z_dtype or (
-        x.dtype if x.dtype in _TYPES else torch.bfloat16)
-    if dt not in _TYPES or x.dtype not in (torch.float32, dt) or gate_act not in _GATES:
-        raise ValueError(f"a {x.dtype} residual with a {dt} branch, gate_act {gate_act!r}")
-    _need(y is None or y.shape == (T, H), "y must be [T][H]")
-    ldg = 0
+        xt if xt in _TYPES else torch.bfloat16)
+    t, act = _TYPES.get(dt), _GATES.get(gate_act)
+    if t is None or act is None or (xt != torch.float32 and xt != dt):
+        raise ValueError(f"a {xt} residual with a {dt} branch, gate_act {gate_act!r}")
+    py = ldy = pg = ldg = 0
+    if y is not None:
+        _need(y.shape == shape, "y must be [T][H]")
+        py, ldy = y.data_ptr(), _rows(y, "y")
     if gate is not None:
-        _need(gate.dtype == dt and tuple(gate.shape) in ((T, H), (1, H), (H,)), "gate must be [T][H] or [H] of the branch's type")
-        ldg = _rows(gate, "gate") if gate.dim() == 2 and gate.shape[0] == T and T > 1 else 0
-        _need(H == 1 or gate.stride(-1) == 1, "gate must have contiguous rows")
-    wt = torch.float32
-    for name, v in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if v is not None:
-            _need(v.shape == (H,) and v.dtype in (torch.float32, dt) and v.is_contiguous(),
-                  f"{name} must be contiguous [H], fp32 or the branch's type")
-            wt = v.dtype
-    _need(post_weight is None or pre_weight is None or post_weight.dtype == pre_weight.dtype, "both weights have one type")
-    _check_cuda(x.device, y=y, gate=gate, post_weight=post_weight, pre_weight=pre_weight, x_out=x_out, z=z)
+        _need(gate.dtype == dt and tuple(gate.shape) in ((T, H), (1, H), (H,)) and (H == 1 or gate.stride(-1) == 1),
+              "gate must be [T][H] or [H] of the branch's type, with contiguous rows")
+        pg, ldg = gate.data_ptr(), _rows(gate, "gate") if gate.dim() == 2 and gate.shape[0] == T and T > 1 else 0
+    wt, pp, pq = B.FLINT_T_F32, 0, 0
+    if post_weight is not None or pre_weight is not None:
+        both = post_weight if post_weight is not None else pre_weight
+        for v in (post_weight, pre_weight):
+            if v is not None and (v.shape != (H,) or v.dtype != both.dtype or not v.is_contiguous()):
+                raise ValueError("the weights must be contiguous [H] of one type")
+        if both.dtype != torch.float32:
+            _need(both.dtype == dt, "the weights must be fp32 or of the branch's type")
+            wt = t
+        pp = 0 if post_weight is None else post_weight.data_ptr()
+        pq = 0 if pre_weight is None else pre_weight.data_ptr()
+    _together(dev, y, gate, post_weight, pre_weight, x_out, z)
     if x_out is None:
-        x_out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+        x_out, ldxo = x.new_empty(shape), H
+    else:
+        _need(x_out.shape == shape and x_out.dtype == xt, "x_out must be [T][H] of x's type")
+        ldxo = _rows(x_out, "x_out")
     if z is None:
-        z = torch.empty((T, H), dtype=dt, device=x.device)
-    _need(x_out.shape == (T, H) and x_out.dtype == x.dtype, "x_out must be [T][H] of x's type")
-    _need(z.shape == (T, H) and z.dtype == dt, "z must be [T][H] of the branch's type")
-    a = B.flint_norm_args(x.data_ptr(), x_out.data_ptr(), _ptr(y), _ptr(gate), _ptr(post_weight), _ptr(pre_weight),
-                          z.data_ptr(), ldx, _rows(x_out, "x_out"), 0 if y is None else _rows(y, "y"), ldg, _rows(z, "z"),
-                          T, H, _TYPES[dt], B.FLINT_T_F32 if x.dtype == torch.float32 else _TYPES[dt],
-                          B.FLINT_T_F32 if wt == torch.float32 else _TYPES[dt], 1 if post_norm else 0, _GATES[gate_act],
-                          res_scale, branch_scale, eps)
-    B.flint_block_norm(a, stream)
+        z, ldz = x.new_empty(shape, dtype=dt), H
+    else:
+        _need(z.shape == shape and z.dtype == dt, "z must be [T][H] of the branch's type")
+        ldz = _rows(z, "z")
+    B.flint_block_norm(B.pack_norm_args(x.data_ptr(), x_out.data_ptr(), py, pg, pp, pq, z.data_ptr(), ldx, ldxo, ldy, ldg, ldz,
+                                        T, H, t, B.FLINT_T_F32 if xt == torch.float32 else t, wt, 1 if post_norm else 0, act,
+                                        res_scale, branch_scale, eps), _stream_of(dev.index))
     return x_out, z
 
 
@@ -256,8 +288,10 @@ class FlintExperts16:
                 scale: float = 1.0, stream=None) -> torch.Tensor:
         """y[t] = scale * sum_k w[t][k] E_ids[t][k](x[t]) + addend[t]: ids int32 [T][top_k] (outside [0, E):
         no expert), w f32 [T][top_k], addend [T][H] (a shared expert's output)."""
+        if _elsewhere(x.device, stream):
+            return _switched(self.forward, x.device, stream, x, ids, w, addend=addend, scale=scale)
         _need(x.dim() == 2 and ids.dim() == 2 and x.shape[0] == ids.shape[0], "x [T][H] and ids [T][top_k]")
-        offsets, perm, inv = expert_permute(ids, self.E, stream=stream)
-        h = grouped_linear(x, self.gate_up, offsets, rows=perm, row_div=ids.shape[1], act="swiglu", stream=stream)
-        o = grouped_linear(h, self.down, offsets, stream=stream)
-        return expert_combine(o, inv, w, addend=addend, scale=scale, stream=stream)
+        offsets, perm, inv = expert_permute(ids, self.E)
+        h = grouped_linear(x, self.gate_up, offsets, rows=perm, row_div=ids.shape[1], act="swiglu")
+        o = grouped_linear(h, self.down, offsets)
+        return expert_combine(o, inv, w, addend=addend, scale=scale)

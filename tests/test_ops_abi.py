@@ -118,6 +118,12 @@ def test_block_norm_limits_and_no_op():
     assert _norm(x_out=0, z=0) == OK
 
 
+def test_packed_norm_arguments_are_the_structure():
+    vals = list(range(1, 8)) + [64, 65, 66, 0, 68] + [4, 64, 0, 2, 2, 1, 1] + [0.5, 2.0, 1e-6]
+    packed = B.pack_norm_args(*vals)
+    assert packed == bytes(B.flint_norm_args(*vals)) and len(packed) == ctypes.sizeof(B.flint_norm_args)
+
+
 def test_error_word_needs_a_place():
     assert B.raw_status("flint_ops_error_word", None) == INVALID
 
