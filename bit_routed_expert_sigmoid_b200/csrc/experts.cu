@@ -4,6 +4,7 @@
 
 #include "kernels.cuh"
 #include "ops.cuh"
+#include "tmap.cuh"
 
 namespace flint {
 
@@ -17,19 +18,18 @@ namespace {
 // depend on the order of the adds); the exclusive scans over the warps of a CTA, the CTAs of the cluster (read
 // through distributed shared memory) and the experts then give each (warp, expert) its first position, and the
 // warp hands out positions 32 pairs at a time by rank among equal ids (match.any). Deterministic throughout.
-constexpr int kPermMaxCtas = 8;                  // portable cluster size
 constexpr int kPermMaxThreads = 1024;
-
-__device__ __forceinline__ int pad32(int i) { return i + (i >> 5); }
+constexpr int kPermMaxE = 1024;                  // one per thread in the scan over the experts
 
 __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const int* __restrict__ ids, int P, int E,
                                                                          int wlen, int* __restrict__ offsets,
                                                                          int* __restrict__ perm, int* __restrict__ inv) {
   extern __shared__ int sm_perm[];
+  __shared__ int wtot[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  int* tot = sm_perm;                            // [pad32(E) + 1] this CTA's pairs per expert
-  int* first = tot + pad32(E) + 1;               // [pad32(E) + 1] cluster totals, then first positions
-  int* cnt = first + pad32(E) + 1;               // [nw][E]
+  int* tot = sm_perm;                            // [E] this CTA's pairs per expert
+  int* first = tot + E;                          // [E + 1] first position of this CTA's pairs; [E] = kept pairs
+  int* cnt = first + E + 1;                      // [nw][E]
   cg::cluster_group cl = cg::this_cluster();
   const int rank = static_cast<int>(cl.block_rank()), ncta = static_cast<int>(cl.num_blocks());
 
@@ -50,51 +50,52 @@ __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const i
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int run = 0;
+#pragma unroll 8
     for (int w = 0; w < nw; ++w) {
       const int c = cnt[w * E + e];
       cnt[w * E + e] = run;
       run += c;
     }
-    tot[pad32(e)] = run;
+    tot[e] = run;
   }
   cl.sync();
-  // cluster totals per expert, and the pairs that CTAs before this one hold
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+  // per expert: the cluster's pairs, and those of the CTAs before this one; then the exclusive scan over the
+  // experts, blockDim of them at a time
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
     int all = 0, before = 0;
-    for (int c = 0; c < ncta; ++c) {
-      const int v = cl.map_shared_rank(tot, c)[pad32(e)];
-      if (c < rank) before += v;
-      all += v;
-    }
-    first[pad32(e)] = all;
-    for (int w = 0; w < nw; ++w) cnt[w * E + e] += before;
-  }
-  cl.sync();                                     // also: nobody reads another CTA's memory behind this
-  if (warp == 0) {                               // exclusive scan over the experts, E/32 neighbours per lane
-    const int per = (E + 31) / 32;
-    int s = 0;
-    for (int j = 0; j < per; ++j)
-      if (lane * per + j < E) s += first[pad32(lane * per + j)];
-    int incl = s;
+    if (e < E)
+      for (int c = 0; c < ncta; ++c) {
+        const int v = cl.map_shared_rank(tot, c)[e];
+        if (c < rank) before += v;
+        all += v;
+      }
+    int incl = all;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
       if (lane >= m) incl += o;
     }
-    int run = incl - s;
-    for (int j = 0; j < per; ++j) {
-      const int e = lane * per + j;
-      if (e < E) {
-        const int c = first[pad32(e)];
-        first[pad32(e)] = run;
-        run += c;
-      }
+    if (lane == 31) wtot[warp] = incl;
+    __syncthreads();
+    int off = base + incl - all, sum = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) off += wtot[w];
+      sum += wtot[w];
     }
-    if (lane == 31) first[pad32(E)] = run;
+    if (e < E) {
+      first[e] = off + before;
+      if (rank == 0) offsets[e] = off;
+    }
+    base += sum;
+    __syncthreads();
   }
-  __syncthreads();
-  if (rank == 0)
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = first[pad32(e)];
+  if (threadIdx.x == 0) {
+    first[E] = base;
+    if (rank == 0) offsets[E] = base;
+  }
+  cl.sync();                                     // nobody reads another CTA's memory behind this
   for (int i0 = lo; i0 < hi; i0 += 128) {
     int v[4];
 #pragma unroll
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const i
       const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
       const int r = __popc(peers & ((1u << lane) - 1u));
       int pos = -1;
-      if (e >= 0) pos = first[pad32(e)] + mine[e] + r;
+      if (e >= 0) pos = first[e] + mine[e] + r;
       __syncwarp();
       if (e >= 0 && r == 0) mine[e] += __popc(peers);
       __syncwarp();
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const i
       }
     }
   }
-  for (long long i = static_cast<long long>(first[pad32(E)]) + rank * blockDim.x + threadIdx.x; i < P;
+  for (long long i = static_cast<long long>(base) + rank * blockDim.x + threadIdx.x; i < P;
        i += static_cast<long long>(ncta) * blockDim.x)
     perm[i] = -1;
 }
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const i
 // once. A thread owns 8 columns (16-byte accesses) or one (any alignment), and issues the loads of 8 slots
 // before their sum, which runs in slot order.
 template <int TYPE, bool VEC>
-__global__ void __launch_bounds__(256) expert_combine_kernel(const __grid_constant__ CombineParams p) {
+__global__ void __launch_bounds__(256, 4) expert_combine_kernel(const __grid_constant__ CombineParams p) {
   constexpr int kCols = VEC ? 8 : 1;
   const long long t = blockIdx.x;
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kCols;
@@ -193,6 +194,34 @@ __global__ void __launch_bounds__(256) expert_combine_kernel(const __grid_consta
   }
 }
 
+// Size of the permutation's cluster: 16 where the device can hold such a one, else the portable 8. More CTAs
+// share the scattered stores.
+int perm_ctas(int dev) {
+  static std::atomic<int> known[kMaxDev];
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  n = 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kPermMaxThreads);
+  cfg.dynamicSmemBytes = 4 * (2 * kPermMaxE + 1 + kPermMaxThreads / 32 * kPermMaxE);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int fits = 0;
+  if (cudaFuncSetAttribute(expert_permute_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&fits, expert_permute_kernel, &cfg) == cudaSuccess && fits > 0)
+    n = 16;
+  else
+    (void)cudaGetLastError();
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <int TYPE>
 cudaError_t launch_combine_type(const CombineParams& p, cudaStream_t s) {
   auto ok = [](const void* q, long long ld) {
@@ -211,18 +240,20 @@ cudaError_t launch_combine_type(const CombineParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, int* perm, int* inv, cudaStream_t s) {
-  const int ncta = P <= 4096 ? 1 : kPermMaxCtas;
+  int dev, sms;
+  cudaError_t err = current_device_sms(&dev, &sms);
+  if (err != cudaSuccess) return err;
+  constexpr int kSmem = 4 * (2 * kPermMaxE + 1 + kPermMaxThreads / 32 * kPermMaxE);
+  if ((err = allow_smem_once<expert_permute_kernel>(dev, kSmem)) != cudaSuccess) return err;
+  const int ncta = P <= 4096 ? 1 : perm_ctas(dev);
   int threads = ((P + ncta - 1) / ncta + 31) / 32 * 32;
   threads = threads < 256 ? 256 : threads > kPermMaxThreads ? kPermMaxThreads : threads;
   const int warps = ncta * (threads / 32);
   const int wlen = ((P + warps - 1) / warps + 31) / 32 * 32;
-  const int smem = 4 * (2 * (E + E / 32 + 1) + threads / 32 * E);
-  cudaError_t e = cudaFuncSetAttribute(expert_permute_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ncta);
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = 4 * (2 * E + 1 + threads / 32 * E);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

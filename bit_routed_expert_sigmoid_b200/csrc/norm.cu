@@ -29,25 +29,34 @@ __device__ __forceinline__ int col_of(int k) {
   else return k * blockDim.x + threadIdx.x;
 }
 
-template <int TYPE, bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* row, int v, int H, float (&out)[8]) {
+// Eight 16-bit elements as they were loaded, in pairs: converted where they are used, so that a row in flight costs
+// few registers.
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int v, int H) {
+  uint4 r = make_uint4(0, 0, 0, 0);
   if constexpr (VEC) {
     const int c = col_of<true>(8 * v);
-    uint4 r = make_uint4(0, 0, 0, 0);
     if (c < H) r = *reinterpret_cast<const uint4*>(row + c);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = pair_to_f32<TYPE>(w[j]);
-      out[2 * j] = f.x;
-      out[2 * j + 1] = f.y;
-    }
   } else {
+    uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = col_of<false>(8 * v + j);
-      out[j] = c < H ? to_f32<TYPE>(row[c]) : 0.f;
+      w[j] = c < H ? row[c] : 0u;
     }
+    r = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+  }
+  return r;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void widen8(const uint4& r, float (&out)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = pair_to_f32<TYPE>(w[j]);
+    out[2 * j] = f.x;
+    out[2 * j + 1] = f.y;
   }
 }
 
@@ -91,59 +100,68 @@ __device__ __forceinline__ void store8(uint16_t* row, int v, int H, const float 
 template <int TYPE, bool VEC>
 __device__ __forceinline__ void load8_weight(const void* w, int w_f32, int v, int H, float (&out)[8]) {
   if (w_f32) load8_f32<VEC>(static_cast<const float*>(w), v, H, out);
-  else load8<TYPE, VEC>(static_cast<const uint16_t*>(w), v, H, out);
+  else widen8<TYPE>(load8<VEC>(static_cast<const uint16_t*>(w), v, H), out);
 }
 
+template <int VPT>
+constexpr int kMaxThreads = VPT == 1 ? 1024 : VPT == 8 ? 512 : 256;
+
+// VPT steps of 8 columns per thread. All of a row's loads are issued before the first reduction.
 template <int TYPE, bool RES_F32, bool VEC, int VPT>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float sum_post[kNormWarps], sum_pre[kNormWarps];
   const long long t = blockIdx.x;
   const int H = p.H;
-  float x[VPT][8], b[VPT][8];
+  float x[VPT][8];
+  uint4 xr[VPT], yr[VPT], gr[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if constexpr (RES_F32) load8_f32<VEC>(static_cast<const float*>(p.x) + t * p.ldx, v, H, x[v]);
-    else load8<TYPE, VEC>(static_cast<const uint16_t*>(p.x) + t * p.ldx, v, H, x[v]);
+    else xr[v] = load8<VEC>(static_cast<const uint16_t*>(p.x) + t * p.ldx, v, H);
+    if (p.y) yr[v] = load8<VEC>(p.y + t * p.ldy, v, H);
+    if (p.gate) gr[v] = load8<VEC>(p.gate + t * p.ldg, v, H);
   }
-  if (p.y) {
-    float g[VPT][8];
+  float norm = 1.f;
+  if (p.post_norm) {
+    float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) load8<TYPE, VEC>(p.y + t * p.ldy, v, H, b[v]);
-    if (p.gate) {
+    for (int v = 0; v < VPT; ++v) {
+      float b[8];
+      widen8<TYPE>(yr[v], b);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) load8<TYPE, VEC>(p.gate + t * p.ldg, v, H, g[v]);
+      for (int j = 0; j < 8; ++j) s = fmaf(b[j], b[j], s);
     }
-    if (p.post_norm) {
-      float s = 0.f;
+    norm = 1.0f / sqrtf(block_sum(s, sum_post) / static_cast<float>(H) + p.eps);
+  }
 #pragma unroll
-      for (int v = 0; v < VPT; ++v)
+  for (int v = 0; v < VPT; ++v) {
+    if constexpr (!RES_F32) widen8<TYPE>(xr[v], x[v]);
+    if (p.y) {
+      float b[8];
+      widen8<TYPE>(yr[v], b);
+      if (p.post_norm) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(b[v][j], b[v][j], s);
-      const float inv = 1.0f / sqrtf(block_sum(s, sum_post) / static_cast<float>(H) + p.eps);
+        for (int j = 0; j < 8; ++j) b[j] *= norm;
+        if (p.post_w) {
+          float w[8];
+          load8_weight<TYPE, VEC>(p.post_w, p.w_f32, v, H, w);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        float w[8];
-        if (p.post_w) load8_weight<TYPE, VEC>(p.post_w, p.w_f32, v, H, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[v][j] = b[v][j] * inv * (p.post_w ? w[j] : 1.0f);
+          for (int j = 0; j < 8; ++j) b[j] *= w[j];
+        }
       }
-    }
-    if (p.gate) {
+      if (p.gate) {
+        float g[8];
+        widen8<TYPE>(gr[v], g);
+        // the fast exponential and division are within a few units of fp32's last place
 #pragma unroll
-      for (int v = 0; v < VPT; ++v)
+        for (int j = 0; j < 8; ++j) b[j] *= p.gate_act == 1 ? __fdividef(1.0f, 1.0f + __expf(-g[j])) : g[j];
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          b[v][j] *= p.gate_act == 1 ? 1.0f / (1.0f + expf(-g[v][j])) : g[v][j];
-    }
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[v][j] = fmaf(p.branch_scale, b[v][j], p.res_scale * x[v][j]);
-  } else {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
+      for (int j = 0; j < 8; ++j) x[v][j] = fmaf(p.branch_scale, b[j], p.res_scale * x[v][j]);
+    } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[v][j] *= p.res_scale;
+    }
   }
   if (p.x_out) {
 #pragma unroll
@@ -187,12 +205,17 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
 
 template <int TYPE, bool RES_F32, bool VEC>
 cudaError_t launch_vpt(const NormParams& p, cudaStream_t s) {
+  // Few rows: a thread per 8 columns, the shortest way through one row. Many rows: up to 4 steps per thread, so that
+  // the reductions cost fewer warps and more loads of more rows are in flight.
   const int n8 = (p.H + 7) / 8;
-  const int vpt = n8 <= 1024 ? 1 : n8 <= 2048 ? 2 : 4;
+  const int vpt = n8 > 1024 ? 8 : p.T >= 1024 && n8 > 512 ? 4 : p.T >= 1024 && n8 > 256 ? 2 : 1;
   const int threads = ((n8 + vpt - 1) / vpt + 31) / 32 * 32;
-  if (vpt == 1) block_norm_kernel<TYPE, RES_F32, VEC, 1><<<p.T, threads, 0, s>>>(p);
-  else if (vpt == 2) block_norm_kernel<TYPE, RES_F32, VEC, 2><<<p.T, threads, 0, s>>>(p);
-  else block_norm_kernel<TYPE, RES_F32, VEC, 4><<<p.T, threads, 0, s>>>(p);
+  switch (vpt) {
+    case 1: block_norm_kernel<TYPE, RES_F32, VEC, 1><<<p.T, threads, 0, s>>>(p); break;
+    case 2: block_norm_kernel<TYPE, RES_F32, VEC, 2><<<p.T, threads, 0, s>>>(p); break;
+    case 4: block_norm_kernel<TYPE, RES_F32, VEC, 4><<<p.T, threads, 0, s>>>(p); break;
+    default: block_norm_kernel<TYPE, RES_F32, VEC, 8><<<p.T, threads, 0, s>>>(p); break;
+  }
   return cudaGetLastError();
 }
 
