@@ -98,6 +98,15 @@ __device__ __forceinline__ GrTile gr_tile(const GrTab& tt, int E, int t) {
   return r;
 }
 
+__device__ __forceinline__ void tma_3d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
+                                            uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(pol)
+      : "memory");
+}
+
 // 16 bytes to shared memory; zeros when !in
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -386,19 +395,35 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
 // ---------------------------------------------------------------------------------------------
 // Few rows (P <= kFewRows): bound by streaming the active groups' weights once. The weight rows of all active
 // groups are cut into units of 16 (SwiGLU: 8 gate rows and their 8 up rows) and spread evenly over one CTA per SM,
-// which a GEMM's 128-row tiles cannot do when a token has six experts. The 16 warps of a CTA split K (128 per step)
-// of a unit, or work on several units when K is short; weights go straight from global memory to the fragments of
-// mma.sync m16n8k16 (8 neighbouring K per lane and load, 64 bytes of a row per four lanes; x is read with the same K
-// order), the next step's loads in flight during this one's products. Partial sums meet in shared memory and are added in warp order.
-constexpr int kFewThreads = 512;
-constexpr int kFewWarps = kFewThreads / 32;
+// which a GEMM's 128-row tiles cannot do when a token has six experts. One thread keeps a ring of stages full: a
+// stage is up to 512 K of the units that the 16 other warps work on, in teams of four warps per unit (fewer when K is
+// short), one TMA box of 8 or 16 KB per unit (half unit with SwiGLU). A warp takes 128 K of a stage and multiplies
+// with mma.sync m16n8k16; any order of K serves as long as both operands have it, so a lane reads 8 neighbouring K at
+// a time and x comes straight from global memory, through L1. A team's partial sums meet in shared memory and are
+// added in warp order; teams do not wait for one another.
+// Small copies starve it: bulk copies of one row (1 or 4 KB) and boxes of 2 KB all streamed ~11 bytes per cycle and
+// SM, boxes of 8 KB and more over twice that.
+constexpr int kFewWarps = 16;                    // consumers; one more warp copies
+constexpr int kFewThreads = 32 * (kFewWarps + 1);
+constexpr int kFewSplit = 4;                     // warps of a team at most: 128 K each per stage
+constexpr int kFewMaxStages = 8;
 
 struct FewTab {
-  int n_active, pad;
-  int wsum[kFewWarps];
+  uint64_t full[kFewMaxStages], empty[kFewMaxStages];
+  int n_active, abort;
+  int wsum[kFewWarps + 1];
   int e[kFewRows], off[kFewRows], cnt[kFewRows];
   int src[kFewRows];                             // row of x of each row of y
 };
+
+struct FewParams {
+  CUtensorMap tm;                                // blocks: [K / 64][E N][64], else [E N][K] (K % 64 != 0)
+  GroupedParams g;
+  int kw;                                        // warps that split a unit's K (a power of two)
+  int stages;
+  int blocks;                                    // 1: one box holds all 64-K blocks of a stage
+};
+constexpr int kFewStage = kFewWarps * 4096;      // 16 rows x 128 K per warp
 
 template <int TYPE>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -409,14 +434,17 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 
 template <int TYPE, int ACT, int NT>
-__global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __grid_constant__ GroupedParams p, int kw_n) {
+__global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __grid_constant__ FewParams ge) {
+  const GroupedParams& p = ge.g;
   constexpr int kUnit = ACT ? 8 : 16;            // outputs per unit
   extern __shared__ uint8_t smem_raw[];
-  float4* red = reinterpret_cast<float4*>(smem_raw);         // [2][kFewWarps][NT][32]
   __shared__ FewTab tab;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int nout = ACT ? p.N / 2 : p.N;
-  const int units_per = (nout + kUnit - 1) / kUnit, segs = (p.K + 127) / 128;
+  const int units_per = (nout + kUnit - 1) / kUnit;
+  const int teams = kFewWarps / ge.kw;
+  uint8_t* ring = align1024(smem_raw);
+  float4* red = reinterpret_cast<float4*>(ring + ge.stages * kFewStage);       // [warps][NT][32]
 
   // active groups in ascending order: thread i looks at the groups 2i, 2i + 1
   int2 span[2];
@@ -435,10 +463,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   }
   if (lane == 31) tab.wsum[warp] = incl;
   if (threadIdx.x < p.P) tab.src[threadIdx.x] = source_row(p, threadIdx.x);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ge.stages; ++i) {
+      mbar_init(&tab.full[i], 1);
+      mbar_init(&tab.empty[i], kFewWarps);
+    }
+    tab.abort = 0;
+    fence_mbar_init();
+  }
   __syncthreads();
   int at = incl - n, total = 0;
 #pragma unroll
-  for (int w = 0; w < kFewWarps; ++w) {
+  for (int w = 0; w <= kFewWarps; ++w) {
     if (w < warp) at += tab.wsum[w];
     total += tab.wsum[w];
   }
@@ -457,84 +493,140 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   const long long units = static_cast<long long>(n_active) * units_per;
   const int u_lo = static_cast<int>(units * blockIdx.x / gridDim.x);
   const int u_hi = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
-  const int kw = warp % kw_n, ul = warp / kw_n, ul_n = kFewWarps / kw_n;
+  const int chunk = 128 * ge.kw, chunks = (p.K + chunk - 1) / chunk;
+  volatile int* abort = &tab.abort;
 
-  uint4 nx[8];                                   // row g: 0..3, row g + 8: 4..7; K = 32 i + 8 q .. + 7 of the step
-  auto load = [&](int u, int s) {
-    const int ai = u / units_per, n0 = (u - ai * units_per) * kUnit + g;
-    const int n1 = ACT ? nout + n0 : n0 + 8;
-    const uint16_t* w = p.w + static_cast<size_t>(tab.e[ai]) * p.N * p.K + s * 128 + 8 * q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = s * 128 + 8 * q + 32 * i < p.K;
-      nx[i] = in && n0 < nout ? ld_stream_v4(w + static_cast<size_t>(n0) * p.K + 32 * i) : make_uint4(0, 0, 0, 0);
-      nx[4 + i] = in && (ACT ? n0 < nout : n1 < nout) ? ld_stream_v4(w + static_cast<size_t>(n1) * p.K + 32 * i)
-                                                      : make_uint4(0, 0, 0, 0);
-    }
-  };
-  if (u_lo + ul < u_hi && kw < segs) load(u_lo + ul, kw);
-  for (int b = 0, u0 = u_lo; u0 < u_hi; ++b, u0 += ul_n) {
-    const int u = u0 + ul;
-    if (u < u_hi && kw < segs) {
-      const int ai = u / units_per, cnt = min(tab.cnt[ai], 8 * NT), off = tab.off[ai];
-      float acc[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
-      for (int s = kw; s < segs; s += kw_n) {
-        uint4 a[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = nx[i];
-        if (s + kw_n < segs) load(u, s + kw_n);
-        else if (u + ul_n < u_hi) load(u + ul_n, kw);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (8 * t < cnt) {
-            const bool tok = 8 * t + g < cnt;
-            const uint16_t* x = p.x + (tok ? tab.src[off + 8 * t + g] * p.ldx : 0) + s * 128 + 8 * q;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (tok && s * 128 + 8 * q + 32 * i < p.K) v = ld_nc_v4(x + 32 * i);
-              mma_16816<TYPE>(acc[t], a[i].x, a[4 + i].x, a[i].y, a[4 + i].y, v.x, v.y);
-              mma_16816<TYPE>(acc[t], a[i].z, a[4 + i].z, a[i].w, a[4 + i].w, v.z, v.w);
+  if (warp == kFewWarps) {
+    // ---- weights
+    if (lane == 0) {
+      const uint64_t pol = l2_evict_first();
+      const int kbs = 2 * ge.kw;                 // 64-K blocks of a stage
+      int it = 0;
+      bool ok = true;
+      for (int u0 = u_lo; u0 < u_hi && ok; u0 += teams) {
+        const int units_now = min(teams, u_hi - u0);
+        for (int c = 0; c < chunks; ++c, ++it) {
+          const int slot = it % ge.stages;
+          if (it >= ge.stages && !pf_wait(&tab.empty[slot], ((it / ge.stages) - 1) & 1, abort, &g_ops_error)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + slot * kFewStage;
+          mbar_arrive_expect_tx(&tab.full[slot], units_now * kbs * 2048);
+          for (int j = 0; j < units_now; ++j, st += kbs * 2048) {
+            const int a = (u0 + j) / units_per;
+            const int r = tab.e[a] * p.N + (u0 + j - a * units_per) * kUnit;
+            if (ge.blocks) {
+              tma_3d_hint(st, &ge.tm, 0, r, c * kbs, &tab.full[slot], pol);
+              if constexpr (ACT) tma_3d_hint(st + kbs * 1024, &ge.tm, 0, r + nout, c * kbs, &tab.full[slot], pol);
+            } else {
+              for (int b = 0; b < kbs; ++b) {    // blocks behind K read as zeros
+                const int x = (c * kbs + b) * 64;
+                tma_2d_hint(st + b * kUnit * 128, &ge.tm, x, r, &tab.full[slot], pol);
+                if constexpr (ACT) tma_2d_hint(st + kbs * 1024 + b * 1024, &ge.tm, x, r + nout, &tab.full[slot], pol);
+              }
             }
           }
         }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        red[(((b & 1) * kFewWarps + warp) * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+      drain_copies(tab.full, ge.stages, it);
     }
-    __syncthreads();                             // one per batch: the other half of red is written next
-    const float* rf = reinterpret_cast<const float*>(red + (b & 1) * kFewWarps * NT * 32);
-    const int parts = min(kw_n, segs);
-    for (int o = threadIdx.x; o < ul_n * 8 * NT * kUnit; o += kFewThreads) {
-      const int j = o % kUnit, tok = (o / kUnit) % (8 * NT), un = o / (kUnit * 8 * NT);
-      if (u0 + un >= u_hi) continue;
-      const int ai = (u0 + un) / units_per, nn = (u0 + un - ai * units_per) * kUnit + j;
-      if (tok >= tab.cnt[ai] || nn >= nout) continue;
-      const int at4 = ((un * kw_n * NT + tok / 8) * 32 + (j & 7) * 4 + (tok & 7) / 2) * 4 + (tok & 1);
-      float r0 = 0.f, r1 = 0.f;
-      for (int w = 0; w < parts; ++w) {
-        r0 += rf[at4 + w * NT * 128 + (ACT ? 0 : (j >> 3) * 2)];
-        if constexpr (ACT) r1 += rf[at4 + w * NT * 128 + 2];
+    return;
+  }
+
+  const int kw = warp % ge.kw, team = warp / ge.kw, tid = kw * 32 + lane;
+  const float* rf = reinterpret_cast<const float*>(red) + team * ge.kw * NT * 128;
+  int it = 0;
+  int ai = (u_lo + team) / units_per, un = u_lo + team - ai * units_per;       // unit `un` of active group ai
+  bool ok = true;
+  for (int u0 = u_lo; u0 < u_hi; u0 += teams) {
+    const bool mine = u0 + team < u_hi;
+    const int cnt = mine ? min(tab.cnt[ai], 8 * NT) : 0, off = mine ? tab.off[ai] : 0;
+    float acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+    for (int c = 0; c < chunks; ++c, ++it) {
+      const int slot = it % ge.stages, k0 = c * chunk + kw * 128 + 8 * q;
+      ok = ok && pf_wait_all(&tab.full[slot], (it / ge.stages) & 1, abort, &g_ops_error);
+      if (mine && ok) {
+        // rows of 128 bytes in the 128-byte swizzle: [64-K block][row], with SwiGLU the gate rows' blocks first
+        const uint8_t* st = ring + slot * kFewStage + team * ge.kw * 4096;
+        const uint8_t* lo = st + kw * 2 * kUnit * 128 + g * 128;
+        const uint8_t* hi = lo + (ACT ? ge.kw * 2048 : 1024);
+        uint4 a[8];                              // row g: 0..3, row g + 8: 4..7; K = k0 + 32 i .. + 7
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = (i >> 1) * kUnit * 128 + (((q + 4 * (i & 1)) ^ g) << 4);
+          a[i] = *reinterpret_cast<const uint4*>(lo + at);
+          a[4 + i] = *reinterpret_cast<const uint4*>(hi + at);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (8 * t < cnt) {
+            const bool tok = 8 * t + g < cnt;
+            const uint16_t* x = p.x + (tok ? tab.src[off + 8 * t + g] * p.ldx : 0) + k0;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};   // two chains
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (tok && k0 + 32 * i < p.K) v = ld_nc_v4(x + 32 * i);
+              mma_16816<TYPE>(acc[t], a[i].x, a[4 + i].x, a[i].y, a[4 + i].y, v.x, v.y);
+              mma_16816<TYPE>(d, a[i].z, a[4 + i].z, a[i].w, a[4 + i].w, v.z, v.w);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][j] += d[j];
+          }
+        }
       }
-      p.y[static_cast<long long>(tab.off[ai] + tok) * p.ldy + nn] = from_f32<TYPE>(ACT ? silu(r0) * r1 : r0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tab.empty[slot]);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (8 * t < cnt) red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    if (named_bar_or(team, 32 * ge.kw, !ok)) break;            // a team gives up together
+    const int j = tid % kUnit, nn = un * kUnit + j;
+    if (nn < nout)
+      for (int tok = tid / kUnit; tok < cnt; tok += 32 * ge.kw / kUnit) {
+        const int at4 = ((tok >> 3) * 32 + (j & 7) * 4 + ((tok & 7) >> 1)) * 4 + (tok & 1);
+        float r0 = 0.f, r1 = 0.f;
+        for (int w = 0; w < ge.kw; ++w) {
+          r0 += rf[at4 + w * NT * 128 + (ACT ? 0 : (j >> 3) * 2)];
+          if constexpr (ACT) r1 += rf[at4 + w * NT * 128 + 2];
+        }
+        p.y[static_cast<long long>(off + tok) * p.ldy + nn] = from_f32<TYPE>(ACT ? silu(r0) * r1 : r0);
+      }
+    named_bar_sync(team, 32 * ge.kw);
+    un += teams;
+    while (un >= units_per) {
+      un -= units_per;
+      ++ai;
     }
   }
 }
 
 template <int TYPE, int ACT, int NT>
 cudaError_t launch_few(const GroupedParams& p, int dev, int sms, cudaStream_t s) {
-  constexpr int smem = 2 * kFewWarps * NT * 32 * 16;
-  cudaError_t e = allow_smem_once<grouped_few_kernel<TYPE, ACT, NT>>(dev, smem);
+  constexpr int kRed = kFewWarps * NT * 512;
+  constexpr int kStages = (226 * 1024 - static_cast<int>(sizeof(FewTab)) - 1024 - kRed) / kFewStage;
+  constexpr int kSmem = kStages * kFewStage + kRed + 1024;
+  static_assert(kStages >= 2 && kStages <= kFewMaxStages, "stages");
+  cudaError_t e = allow_smem_once<grouped_few_kernel<TYPE, ACT, NT>>(dev, kSmem);
   if (e != cudaSuccess) return e;
-  const int segs = (p.K + 127) / 128;
-  int kw = 1;
-  while (kw < segs && kw < kFewWarps) kw *= 2;
-  grouped_few_kernel<TYPE, ACT, NT><<<sms, kFewThreads, smem, s>>>(p, kw);
+  FewParams fp;
+  fp.g = p;
+  fp.kw = 1;
+  while (fp.kw * 128 < p.K && fp.kw < kFewSplit) fp.kw *= 2;
+  fp.stages = kStages;
+  fp.blocks = p.K % 64 == 0;
+  const uint64_t rows = static_cast<uint64_t>(p.E) * p.N;
+  const uint32_t box = ACT ? 8 : 16;
+  if (!(fp.blocks ? encode_16bit_blocks(&fp.tm, p.w, TYPE == kTBf16, rows, p.K, p.K, box, 2 * fp.kw)
+                  : encode_16bit(&fp.tm, p.w, TYPE == kTBf16, rows, p.K, p.K, box)))
+    return cudaErrorInvalidValue;
+  grouped_few_kernel<TYPE, ACT, NT><<<sms, kFewThreads, kSmem, s>>>(fp);
   return cudaGetLastError();
 }
 

@@ -41,6 +41,21 @@ inline bool encode_16bit(CUtensorMap* m, const void* base, bool bf16, uint64_t r
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same matrix (cols a multiple of 64) as [cols / 64][rows][64], with boxes of blocks x box_rows x 64 in the
+// 128-byte swizzle: several 64-column blocks of a few rows by one instruction.
+inline bool encode_16bit_blocks(CUtensorMap* m, const void* base, bool bf16, uint64_t rows, uint64_t cols, uint64_t ld,
+                                uint32_t box_rows, uint32_t blocks) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {64, rows, cols / 64};
+  const cuuint64_t strides[2] = {ld * 2, 128};
+  const cuuint32_t box[3] = {64, box_rows, blocks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDev = 64;
 
 // SM count of the current device (looked up once per device), and the device's index.
