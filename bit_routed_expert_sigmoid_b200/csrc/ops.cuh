@@ -1,6 +1,8 @@
 // Kernel launchers of the standalone operators (internal interface between ops_api.cu and the device code).
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace flint {
@@ -36,7 +38,8 @@ struct GroupedParams {
   long long ldy;
 };
 cudaError_t launch_grouped_linear(const GroupedParams& p, cudaStream_t s);
-cudaError_t read_ops_error(unsigned* out);       // of the current device; waits for it, clears the word
+cudaError_t read_ops_error(unsigned* out);       // of the current device; waits for it, clears the words
+cudaError_t read_q4_error(unsigned* out);
 
 cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, int* perm, int* inv, cudaStream_t s);
 
@@ -69,6 +72,15 @@ struct NormParams {
   float res_scale, branch_scale, eps;
 };
 cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s);
+
+__device__ __forceinline__ void tma_3d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
+                                            uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(pol)
+      : "memory");
+}
 
 // 16-bit element of an activation tensor as fp32, and back (one rounding, to nearest even)
 template <int TYPE>

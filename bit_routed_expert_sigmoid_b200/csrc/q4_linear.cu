@@ -1,342 +1,629 @@
 // Linear products with 4-bit weights for few tokens (flint_q4_linear):
 //   y[t][n] = ts * sum over 128-segments of  s[n] * (code[n] . x'[t]),  x' = x or blockdiag(Hn) x.
 //
-// Bound by streaming the weights once. The rows of W are spread evenly over one CTA per SM (not in units of a
-// tile), and the 16 warps of a CTA split K: a warp takes a 128-segment of up to 16 RB rows straight from global
-// memory into the fragments of mma.sync m16n8k16 (a lane's 16 bytes are 32 neighbouring K of one row; x is stored
-// in the same order), the next segment's loads in flight during this one's products. Codes become exact fp16
-// (int4: -8..7; NVFP4: E2M1 x E4M3, six significant bits); the int4 group scale multiplies the segment's fp32 sum.
+// Bound by streaming the weights once, and close behind it by the instructions that decode them. The rows of W are
+// divided evenly over one CTA per SM (not in units of a tile); 16 warps split K: a warp takes a 128-segment of up to RB
+// blocks of up to 16 rows at a time, as fragments of mma.sync. A fragment's K order is free as long as x has the same:
+// a lane's 16 bytes are 32 neighbouring K of one row.
 //
-// x' enters as fp16 with one power of two per (token, segment) that brings the segment's largest finite value into
-// [2^14, 2^15): 16-bit inputs stay exact down to 2^-29 of that value (2^-38 absolute), rotated ones are rounded to
-// fp16's 11 bits, and the factor is taken out of the fp32 sum, so no range is lost for either type. With few
-// (token, segment) pairs every CTA builds this operand itself in shared memory; with more, one kernel builds it
-// once in the workspace and the product kernel, launched behind it as a programmatic dependent, starts its weight
-// loads meanwhile.
+// How codes meet x, per 128-segment (Arith):
+//   kExactF16  int4 without rotation, NVFP4: codes become exact fp16 (int4: -8..7; NVFP4: E2M1 x E4M3, six significant
+//              bits); x is fp16 after one power of two per (token, segment) that brings the segment's largest finite
+//              value into [2^14, 2^15): 16-bit inputs stay exact down to 2^-29 of it (2^-38 absolute). The factor is
+//              taken out of the fp32 sum again, so no range is lost for either type.
+//   kLimbs     rotated int4: Hn x is rounded to 16-bit fixed point per (token, segment), a unit being 2^-14 of the power
+//              of two below the segment's largest value (rotation spreads outliers, so that is finer than fp16 for all
+//              but the smallest values); its signed high and unsigned low bytes multiply the exact int8 16 c on the
+//              integer tensor cores. Three instructions decode eight codes instead of nine (8192 x 8192, T = 8: see
+//              launch_ring).
+// The int4 group scale multiplies the segment's sum in fp32.
+//
+// With few segments every CTA builds the operand itself in shared memory; with more, one kernel builds it once in the
+// workspace and the product kernel, launched behind it as a programmatic dependent, starts its weight copies meanwhile.
 #include "kernels.cuh"
 #include "ops.cuh"
+#include "tc.cuh"
 #include "tmap.cuh"
 
 namespace flint {
+
+__device__ unsigned g_ops_error_q4;              // timeout bits of bounded waits (flint_ops_error_word)
 
 namespace {
 
 constexpr int kQ4Threads = 512;
 constexpr int kQ4Warps = kQ4Threads / 32;
-// (token, segment) pairs up to which each CTA builds the operand itself (8 per warp)
-constexpr int kQ4Inline = 128;
-constexpr size_t kQ4InlineBytes = 150 * 1024;    // beside at most 64 KB of partial sums
+// Segments up to which each CTA builds the operand of up to 8 tokens itself (at most 8 pairs per warp and 33 KB)
+constexpr int kQ4Inline = 16;
 
-// The operand of one (token tile of 8, segment): [i 0..3][lane][8 halves], lane = 4 (token % 8) + q holding
-// K = 32 q + 8 i .. + 7 of the segment in the order of the decoded pairs, and the eight inverse factors.
+enum Arith : int { kExactF16Int4, kExactF16Nvfp4, kLimbs };
+
+// The operand of one (token, segment): four chunks of 16 bytes for each of the four lanes q that read it, K = 32 q ..
+// 32 q + 31. fp16: chunk i holds K = 32 q + 8 i .. + 7 in the order of the decoded pairs; limbs: chunk 2 limb + (i >> 1)
+// holds at 8 (i & 1) the bytes of K = 32 q + 8 i + 0, 2, 4, 6 and of + 1, 3, 5, 7.
+// Up to 8 tokens (the ring kernel copies what is there): [segment][token][chunk][q], then the inverse factor, kTokenBytes
+// each. More tokens: [segment][tile of 8][chunk][token][q], so that a warp's loads are contiguous, and behind all of
+// them the factors [segment][tile][8].
+constexpr int kTokenBytes = 272;
 constexpr int kTileBytes = 2048;
 
-__host__ __device__ inline size_t q4_operand_bytes(int tiles, int segs) {
-  return static_cast<size_t>(tiles) * segs * (kTileBytes + 32);
+__host__ __device__ inline size_t q4_operand_bytes(int T, int segs) {
+  return T <= 8 ? static_cast<size_t>(T) * segs * kTokenBytes : static_cast<size_t>((T + 7) / 8) * segs * (kTileBytes + 32);
 }
 
-// One (token, segment) by one warp. img: the operand of (tile 0, segment 0), indexed [segment][tile].
-template <int FMT, int TYPE>
-__device__ __forceinline__ void q4_operand(const Q4Params& p, int t, int seg, int tile, int tiles, uint8_t* img, float* fac) {
-  const int lane = threadIdx.x & 31;
-  const int k = seg * 128 + 4 * lane;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (k < p.K) {                                 // K is a multiple of 16: four neighbours are in or out together
-    const uint2 r = __ldg(reinterpret_cast<const uint2*>(p.x + t * p.ldx + k));
-    const float2 a = pair_to_f32<TYPE>(r.x), b = pair_to_f32<TYPE>(r.y);
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+struct OperandPlace {
+  uint8_t* at;                                   // of chunk 0, q = 0
+  int chunk;                                     // bytes from a chunk to the next
+  float* factor;
+};
+
+__device__ __forceinline__ OperandPlace q4_place(uint8_t* img, int t, int seg, int T, int segs) {
+  OperandPlace o;
+  if (T <= 8) {
+    o.at = img + (static_cast<size_t>(seg) * T + t) * kTokenBytes;
+    o.chunk = 64;
+    o.factor = reinterpret_cast<float*>(o.at + 256);
+  } else {
+    const size_t tiles = (T + 7) / 8, tile = seg * tiles + (t >> 3);
+    o.at = img + tile * kTileBytes + (t & 7) * 64;
+    o.chunk = 512;
+    o.factor = reinterpret_cast<float*>(img + tiles * segs * kTileBytes) + tile * 8 + (t & 7);
   }
-  if (FMT == kInt4 && p.rotated) fwht128_warp(v);
+  return o;
+}
+
+// A warp's four elements per lane of one (token, segment).
+__device__ __forceinline__ uint2 q4_fetch(const Q4Params& p, int t, int seg) {
+  const int k = seg * 128 + 4 * (threadIdx.x & 31);
+  // K is a multiple of 16: four neighbours are in or out together
+  return k < p.K ? __ldg(reinterpret_cast<const uint2*>(p.x + t * p.ldx + k)) : make_uint2(0, 0);
+}
+
+// The operand of one (token, segment) by one warp.
+template <int AR, int TYPE>
+__device__ __forceinline__ void q4_operand(const uint2& raw, const OperandPlace& o) {
+  const int lane = threadIdx.x & 31;
+  const float2 v01 = pair_to_f32<TYPE>(raw.x), v23 = pair_to_f32<TYPE>(raw.y);
+  float v[4] = {v01.x, v01.y, v23.x, v23.y};
+  if constexpr (AR == kLimbs) fwht128_warp(v);
   uint32_t m = 0;
+  bool odd_ones = false;                         // infinities or NaN
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    if (a < 0x7F800000u) m = max(m, a);          // finite ones only: infinities and NaN pass through as they are
+    if (a < 0x7F800000u) m = max(m, a);
+    else odd_ones = true;
   }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   const int e = min(max(static_cast<int>(m >> 23), 15), 254);      // biased exponent of the largest value
   const float f = m ? __uint_as_float(static_cast<uint32_t>(268 - e) << 23) : 1.f;     // 2^(141 - e)
-  const float inv = m ? __uint_as_float(static_cast<uint32_t>(e - 14) << 23) : 1.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] *= f;
-  uint8_t* at = img + (static_cast<size_t>(seg) * tiles + tile) * kTileBytes +
-                (((lane >> 1) & 3) * 32 + (t & 7) * 4 + (lane >> 3)) * 16 + 8 * (lane & 1);
+  float inv = m ? __uint_as_float(static_cast<uint32_t>(e - 14) << 23) : 1.f;
+  uint8_t* at = o.at + (lane >> 3) * 16;
+  const int i = (lane >> 1) & 3;
+  const bool odd = lane & 1;
   uint2 u;
-  if constexpr (FMT == kInt4) {                  // 8-block order 0,4,1,5,2,6,3,7: see int4x8_to_half2x4
-    const bool odd = lane & 1;
-    const float r0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[2], 1);
-    const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[1] : v[3], 1);
-    u = odd ? make_uint2(pack_half2(r0, v[2]), pack_half2(r1, v[3])) : make_uint2(pack_half2(v[0], r0), pack_half2(v[1], r1));
+  if constexpr (AR == kLimbs) {
+    uint32_t hi = 0, lo = 0;                     // bytes 0, 1: elements 0, 2; bytes 2, 3: elements 1, 3
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = min(__float2int_rn(v[j] * f), 32767);
+      const int sh = 8 * ((j >> 1) + 2 * (j & 1));
+      hi |= (static_cast<uint32_t>(n >> 8) & 0xFFu) << sh;
+      lo |= (static_cast<uint32_t>(n) & 0xFFu) << sh;
+    }
+    // the even lane of a pair writes the high limbs of the eight, the odd lane the low ones
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? hi : lo, 1);
+    const uint32_t first = odd ? got : hi, second = odd ? lo : got;
+    u = make_uint2(__byte_perm(first, second, 0x5410), __byte_perm(first, second, 0x7632));
+    at += (2 * odd + (i >> 1)) * o.chunk + (i & 1) * 8;
+    inv *= 0.0625f;                              // the codes enter as 16 c
+    // what is infinite or no number stays so, for the token's whole sum
+    if (__any_sync(0xFFFFFFFFu, odd_ones)) inv = __uint_as_float(0x7FC00000u);
   } else {
-    u = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= f;       // infinities and NaN pass through as they are
+    if constexpr (AR == kExactF16Int4) {         // 8-block order 0,4,1,5,2,6,3,7: see int4x8_to_half2x4
+      const float r0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[2], 1);
+      const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[1] : v[3], 1);
+      u = odd ? make_uint2(pack_half2(r0, v[2]), pack_half2(r1, v[3])) : make_uint2(pack_half2(v[0], r0), pack_half2(v[1], r1));
+    } else {
+      u = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+    }
+    at += i * o.chunk + 8 * odd;
   }
   *reinterpret_cast<uint2*>(at) = u;
-  if (lane == 0) fac[(static_cast<size_t>(seg) * tiles + tile) * 8 + (t & 7)] = inv;
+  if (lane == 0) *o.factor = inv;
 }
 
-template <int FMT, int TYPE>
+template <int AR, int TYPE>
 __global__ void __launch_bounds__(256) q4_operand_kernel(const __grid_constant__ Q4Params p) {
   pdl_trigger();                                 // the product kernel waits for this one before it reads the operand
-  const int segs = (p.K + 127) / 128, tiles = (p.T + 7) / 8;
-  uint8_t* img = static_cast<uint8_t*>(p.workspace);
-  float* fac = reinterpret_cast<float*>(img + static_cast<size_t>(tiles) * segs * kTileBytes);
+  const int segs = (p.K + 127) / 128;
   for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < static_cast<long long>(p.T) * segs;
        i += static_cast<long long>(gridDim.x) * 8) {
     const int t = static_cast<int>(i / segs), seg = static_cast<int>(i - static_cast<long long>(t) * segs);
-    q4_operand<FMT, TYPE>(p, t, seg, t >> 3, tiles, img, fac);
+    q4_operand<AR, TYPE>(q4_fetch(p, t, seg), q4_place(static_cast<uint8_t*>(p.workspace), t, seg, p.T, segs));
   }
 }
 
-// Rows g and g + 8 of a block: this lane's 16 bytes of codes and its scales.
-struct Q4Frag {
-  uint4 c[2];
-  uint32_t s[2];
-};
+// ---------------------------------------------------------------------------------------------
+// fragments
 
-// n[h]: the lane's two rows, behind the row `base` points at.
-template <int FMT, bool WIDE>
-__device__ __forceinline__ void q4_load(const Q4Params& p, const uint8_t* codes, const uint8_t* scales, const int (&n)[2],
-                                        int seg, Q4Frag& f) {
-  const int q = threadIdx.x & 3;
+// One row's 32 codes (16 bytes) as fp16 pairs, the order of the fp16 operand; s2: the two block scales (NVFP4).
+template <int AR>
+__device__ __forceinline__ void decode_f16(const uint4& c, uint32_t s2, uint32_t (&d)[16]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int k = seg * 128 + 32 * q;
-    const uint8_t* c = codes + static_cast<uint32_t>(n[h]) * static_cast<uint32_t>(p.K >> 1) + (k >> 1);
-    if constexpr (FMT == kInt4) {
-      f.c[h] = ld_stream_v4(c);
-      f.s[h] = __ldg(reinterpret_cast<const uint16_t*>(scales) + static_cast<uint32_t>(n[h]) * static_cast<uint32_t>(p.K >> 7) + seg);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (AR == kExactF16Int4) {
+      uint32_t pr[4];
+      int4x8_to_half2x4(w[i], pr);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = pr[j];
     } else {
-      const uint8_t* s = scales + static_cast<uint32_t>(n[h]) * static_cast<uint32_t>(p.K >> 4) + (k >> 4);
-      f.c[h] = make_uint4(0, 0, 0, 0);
-      f.s[h] = 0;
-      if constexpr (WIDE) {                      // K a multiple of 32: codes in 16 bytes, both scales in one load
-        if (k < p.K) {
-          f.c[h] = ld_stream_v4(c);
-          f.s[h] = __ldg(reinterpret_cast<const uint16_t*>(s));
-        }
-      } else {
-        if (k < p.K) {
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(c));
-          f.c[h].x = a.x, f.c[h].y = a.y;
-          f.s[h] = __ldg(s);
-        }
-        if (k + 16 < p.K) {
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(c + 8));
-          f.c[h].z = a.x, f.c[h].w = a.y;
-          f.s[h] |= static_cast<uint32_t>(__ldg(s + 1)) << 8;
-        }
-      }
+      const uint32_t h = e4m3_to_half_bits((s2 >> (8 * (i >> 1))) & 0xFFu);
+      const uint32_t hh = h | (h << 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[4 * i + j] = hmul2_u32(e2m1x2_to_half2(w[i] >> (8 * j)), hh);
     }
   }
 }
 
-// The 32 codes of each of the two rows as fp16 pairs: a[w][j] of row h in d[h][4 w + j].
-template <int FMT>
-__device__ __forceinline__ void q4_decode(const Q4Frag& f, uint32_t (&d)[2][16]) {
+// d += A B on the integer tensor cores (m16n8k32): A s8, B s8 or u8
+template <bool SIGNED_B>
+__device__ __forceinline__ void mma_s8_16832(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (SIGNED_B)
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The codes of rows g and g + 8 (a lane's 16 bytes each) as the A operand of one segment.
+template <int AR>
+struct AFrag {
+  uint32_t a[2][16];
+  __device__ __forceinline__ void decode(const uint4 (&c)[2], const uint32_t (&s)[2]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w[4] = {f.c[h].x, f.c[h].y, f.c[h].z, f.c[h].w};
+    for (int h = 0; h < 2; ++h) decode_f16<AR>(c[h], s[h], a[h]);
+  }
+  // sums over the segment of the lane's two rows (0, 1: row g, tokens 2q and 2q + 1; 2, 3: row g + 8), two chains
+  __device__ __forceinline__ void times(const uint4 (&x)[4], float (&d)[4]) const {
+    float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (FMT == kInt4) {
-        uint32_t pr[4];
-        int4x8_to_half2x4(w[i], pr);
+      const uint32_t m0[4] = {a[0][4 * i], a[1][4 * i], a[0][4 * i + 1], a[1][4 * i + 1]};
+      const uint32_t m1[4] = {a[0][4 * i + 2], a[1][4 * i + 2], a[0][4 * i + 3], a[1][4 * i + 3]};
+      mma_f16_16816(d, m0, x[i].x, x[i].y);
+      mma_f16_16816(e, m1, x[i].z, x[i].w);
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[h][4 * i + j] = pr[j];
-      } else {
-        const uint32_t s = e4m3_to_half_bits((f.s[h] >> (8 * (i >> 1))) & 0xFFu);
-        const uint32_t s2 = s | (s << 16);
+    for (int j = 0; j < 4; ++j) d[j] += e[j];
+  }
+};
+
+template <>
+struct AFrag<kLimbs> {
+  uint32_t even[2][4], odd[2][4];                // int8 16 c: nibbles 0, 2, 4, 6 and 1, 3, 5, 7 of a word
+  __device__ __forceinline__ void decode(const uint4 (&c)[2], const uint32_t (&)[2]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[h][4 * i + j] = hmul2_u32(e2m1x2_to_half2(w[i] >> (8 * j)), s2);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        even[h][i] = (w[i] << 4) & 0xF0F0F0F0u;
+        odd[h][i] = w[i] & 0xF0F0F0F0u;
       }
     }
   }
-}
-
-// NT token tiles of 8 and RB blocks of 16 rows at a time; kw_n warps split K, kQ4Warps / kw_n of such teams take
-// different rows.
-template <int FMT, int TYPE, int NT, int RB, bool WIDE, bool INLINE>
-__global__ void __launch_bounds__(kQ4Threads, 1) q4_linear_kernel(const __grid_constant__ Q4Params p, int kw_n) {
-  extern __shared__ uint8_t sm[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int segs = (p.K + 127) / 128, kw = warp % kw_n, team = warp / kw_n, teams = kQ4Warps / kw_n;
-  const int t0 = blockIdx.y * 8 * NT, tiles_all = INLINE ? NT : (p.T + 7) / 8;
-  const int ntile = min(NT, (p.T - t0 + 7) / 8);
-  float4* red = reinterpret_cast<float4*>(sm);   // [warps][RB][NT][32]
-  const uint8_t* img;
-  if constexpr (INLINE) img = sm + kQ4Warps * RB * NT * 512;
-  else img = static_cast<const uint8_t*>(p.workspace);
-  const float* fac = reinterpret_cast<const float*>(img + static_cast<size_t>(tiles_all) * segs * kTileBytes);
-
-  // the CTA's rows [lo, lo + rows) in blocks of at most 16 and nearly equal size, a multiple of RB per team; lanes
-  // behind the end of a block repeat its last row (the same sectors), their results are not used
-  const int lo = static_cast<int>(static_cast<long long>(p.N) * blockIdx.x / gridDim.x);
-  const int rows = static_cast<int>(static_cast<long long>(p.N) * (blockIdx.x + 1) / gridDim.x) - lo;
-  const int round = teams * RB, blocks = ((rows + 15) / 16 + round - 1) / round * round;
-  const int per = rows / blocks, more = rows % blocks;              // blocks of per + 1 rows, then of per
-  auto block_row = [&](int b) { return b * per + min(b, more); };
-  const uint8_t* codes = p.codes + static_cast<size_t>(lo) * (p.K >> 1);
-  const uint8_t* scales = p.scales + static_cast<size_t>(lo) * (FMT == kInt4 ? p.K >> 6 : p.K >> 4);
-
-  int n[RB][2];
-  auto rows_of = [&](int b0) {
+  // |256 hi + lo| <= 128 * 128 * 2^15 < 2^31: exact
+  __device__ __forceinline__ void times(const uint4 (&x)[4], float (&d)[4]) const {
+    int hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const int first = block_row(b0 + r), last = max(block_row(b0 + r + 1) - 1, 0);
-      n[r][0] = min(first + g, last);
-      n[r][1] = min(first + g + 8, last);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m[4] = {even[0][i], even[1][i], odd[0][i], odd[1][i]};
+      const uint4& xh = x[i >> 1];
+      const uint4& xl = x[2 + (i >> 1)];
+      mma_s8_16832<true>(hi, m, i & 1 ? xh.z : xh.x, i & 1 ? xh.w : xh.y);
+      mma_s8_16832<false>(lo, m, i & 1 ? xl.z : xl.x, i & 1 ? xl.w : xl.y);
     }
-  };
-  Q4Frag f[RB];
-  rows_of(team * RB);
-  if (kw < segs) {
 #pragma unroll
-    for (int r = 0; r < RB; ++r) q4_load<FMT, WIDE>(p, codes, scales, n[r], kw, f[r]);
+    for (int j = 0; j < 4; ++j) d[j] = static_cast<float>(hi[j] * 256 + lo[j]);
   }
-  if constexpr (INLINE) {
-    for (int i = warp; i < p.T * segs; i += kQ4Warps) {       // one token chunk: t0 is 0
-      const int t = i / segs, seg = i - t * segs;
-      q4_operand<FMT, TYPE>(p, t, seg, t >> 3, NT, const_cast<uint8_t*>(img), const_cast<float*>(fac));
+};
+
+// ---------------------------------------------------------------------------------------------
+// The product, codes streamed by TMA: one thread keeps a ring of stages full, a stage being 128 K per warp of a team
+// for RB blocks of R rows per team. Blocks have the same R <= 16 rows everywhere (the rows of W divided evenly over the
+// SMs), which is the height of the TMA box, so no row is read twice; a box holds all 256-code blocks of a stage (K a
+// multiple of 256), or one of them. Rows are 128 bytes in the 128-byte swizzle, counted from the 1024-byte aligned
+// ring. NVFP4 rows that are no multiple of 16 bytes (K % 32 = 16) have no tensor map: the warps read them themselves
+// (TMA = false; the same blocks and order).
+// Whatever a step needs comes through the ring, x and (where their rows are multiples of 16 bytes) the scales too: an
+// ordinary load issued behind 150 KB of copies waits for all of them, which cost 5 us of 17 at 8192 x 8192, T = 8, for
+// x and for the scales each.
+constexpr int kRingThreads = kQ4Threads + 32;
+constexpr int kRingMaxStages = 8;
+constexpr int kQ4Split = 8;                      // warps of a team: two teams of 8 use a stage's x twice
+constexpr int kQ4ScaleBytes = 48 * 1024;         // scales kept in shared memory at most
+
+struct RingParams {
+  CUtensorMap tm;                                // boxed: [K / 256][N][128 bytes], else [N][K / 2 bytes]
+  Q4Params q;
+  int kw;                                        // warps of a team
+  int R;                                         // rows of a block
+  int blocks;                                    // blocks per CTA, a multiple of RB * teams
+  int stages, boxed;
+  int scale_bytes;                               // of the CTA's rows, kept in shared memory; 0: loaded when needed
+};
+
+struct RingBars {
+  uint64_t full[kRingMaxStages], empty[kRingMaxStages], scales;
+  int abort;
+};
+
+// Bytes of a block's rows in a stage: whole swizzle atoms, so that a lane's place in them is the same in every block.
+__host__ __device__ inline int ring_region(int kw, int R) { return ((kw + 1) / 2 * R * 128 + 1023) & ~1023; }
+
+template <int AR, int TYPE, int NT, int RB, bool TMA, bool INLINE>
+__global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_constant__ RingParams rp) {
+  const Q4Params& p = rp.q;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ RingBars bb;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int segs = (p.K + 127) / 128, teams = kQ4Warps / rp.kw, chunks = (segs + rp.kw - 1) / rp.kw;
+  constexpr bool kXRing = TMA && NT == 1 && !INLINE;             // x through the ring
+  const int R = rp.R, kbs = (rp.kw + 1) / 2, region = ring_region(rp.kw, R);
+  const int xstage = kXRing ? rp.kw * p.T * kTokenBytes : 0;
+  const int stage = (teams * RB * region + xstage + 1023) & ~1023;
+  const int total = (p.N + R - 1) / R, first = blockIdx.x * rp.blocks, rounds = rp.blocks / (teams * RB);
+  constexpr bool kI4 = AR != kExactF16Nvfp4;
+  const size_t scale_row = kI4 ? p.K >> 6 : p.K >> 4;            // bytes
+  uint8_t* ring = align1024(smem_raw);
+  float4* red = reinterpret_cast<float4*>(ring + rp.stages * stage);           // [warps][RB][NT][32]
+  uint8_t* sm_scales = reinterpret_cast<uint8_t*>(red + kQ4Warps * RB * NT * 32);
+  uint8_t* sm_x = sm_scales + rp.scale_bytes;                    // INLINE: the operand
+  volatile int* abort = &bb.abort;
+
+  if constexpr (TMA) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < rp.stages; ++i) {
+        mbar_init(&bb.full[i], kXRing ? 2 : 1);
+        mbar_init(&bb.empty[i], kQ4Warps);
+      }
+      mbar_init(&bb.scales, 1);
+      bb.abort = 0;
+      fence_mbar_init();
     }
     __syncthreads();
-  } else {
+  }
+  if (warp == kQ4Warps) {
+    if (TMA && lane == 0) {
+      // weights are no predecessor's output: copied before griddepcontrol.wait; x is the operand kernel's
+      const uint64_t pol = l2_evict_first();
+      const int steps = rounds * chunks;
+      const uint8_t* img = static_cast<const uint8_t*>(p.workspace);
+      auto copy_x = [&](int it, int slot) {
+        const int c = it % chunks, n = min(rp.kw, segs - c * rp.kw) * p.T * kTokenBytes;
+        mbar_arrive_expect_tx(&bb.full[slot], n);
+        bulk_g2s(ring + slot * stage + teams * RB * region, img + static_cast<size_t>(c) * rp.kw * p.T * kTokenBytes, n,
+                 &bb.full[slot]);
+      };
+      auto copy_codes = [&](int it, int slot) {
+        const int rd = it / chunks, c = it - rd * chunks, b0 = first + rd * teams * RB, n = min(teams * RB, total - b0);
+        uint8_t* st = ring + slot * stage;
+        mbar_arrive_expect_tx(&bb.full[slot], max(n, 0) * kbs * R * 128);
+        for (int j = 0; j < n; ++j, st += region) {
+          if (rp.boxed) {
+            tma_3d_hint(st, &rp.tm, 0, (b0 + j) * R, c * kbs, &bb.full[slot], pol);
+          } else {
+            for (int b = 0; b < kbs; ++b)
+              tma_2d_hint(st + b * R * 128, &rp.tm, (c * kbs + b) * 32, (b0 + j) * R, &bb.full[slot], pol);
+          }
+        }
+      };
+      if (rp.scale_bytes) {
+        const int rows = min(rp.blocks * R, p.N - first * R);
+        mbar_arrive_expect_tx(&bb.scales, rows * static_cast<int>(scale_row));
+        bulk_g2s_hint(sm_scales, p.scales + first * R * scale_row, rows * static_cast<int>(scale_row), &bb.scales, pol);
+      }
+      int it = 0;
+      const int ahead = min(rp.stages, steps);
+      for (; it < ahead; ++it) copy_codes(it, it);
+      if constexpr (kXRing) {
+        pdl_wait();
+        for (int j = 0; j < ahead; ++j) copy_x(j, j);
+      }
+      for (; it < steps; ++it) {
+        const int slot = it % rp.stages;
+        if (!pf_wait(&bb.empty[slot], ((it / rp.stages) - 1) & 1, abort, &g_ops_error_q4)) break;
+        if constexpr (kXRing) copy_x(it, slot);
+        copy_codes(it, slot);
+      }
+      // no copy in flight when the CTA exits
+      for (int j = max(it - rp.stages, 0); j < it; ++j)
+        mbar_wait_bounded(&bb.full[j % rp.stages], (j / rp.stages) & 1, 1000000);
+      if (rp.scale_bytes) mbar_wait_bounded(&bb.scales, 0, 1000000);
+    }
+    return;
+  }
+
+  const int kw = warp % rp.kw, team = warp / rp.kw, tid = kw * 32 + lane;
+  const int t0 = blockIdx.y * 8 * NT, tiles = (p.T + 7) / 8;
+  const int ntile = min(NT, (p.T - t0 + 7) / 8);
+  const uint8_t* img = static_cast<const uint8_t*>(p.workspace);
+  const float* fac = reinterpret_cast<const float*>(img + static_cast<size_t>(tiles) * segs * kTileBytes);
+
+  // the lane's place in a block: row g + 8 h (the last one repeated behind the block's end), its 16 bytes
+  uint32_t place[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t row = (kw >> 1) * R + min(g + 8 * h, R - 1);
+    place[h] = team * RB * region + row * 128 + (((4 * (kw & 1) + q) ^ (row & 7)) << 4);
+  }
+  // scales of the lane's rows (NVFP4: of its two 16-blocks), one step ahead of their use; rows behind N repeat the last
+  const uint8_t* scales = p.scales + first * R * scale_row + (kI4 ? 0 : 2 * q);
+  uint32_t srow[RB][2];                          // behind the CTA's first row
+  auto scale_rows = [&](int rd) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = min(((rd * teams + team) * RB + r) * R + min(g + 8 * h, R - 1), p.N - 1 - first * R);
+        srow[r][h] = static_cast<uint32_t>(row) * static_cast<uint32_t>(scale_row);
+      }
+  };
+  uint32_t sc[RB][2];
+  auto load_scales = [&](int seg) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (kI4) {
+          sc[r][h] = __ldg(reinterpret_cast<const uint16_t*>(scales + (srow[r][h] + 2 * seg)));
+        } else if constexpr (TMA) {
+          sc[r][h] = seg * 128 + 32 * q < p.K ? __ldg(reinterpret_cast<const uint16_t*>(scales + (srow[r][h] + 8 * seg))) : 0u;
+        } else {
+          sc[r][h] = seg * 128 + 32 * q < p.K ? __ldg(scales + (srow[r][h] + 8 * seg)) : 0u;
+          if (seg * 128 + 32 * q + 16 < p.K) sc[r][h] |= static_cast<uint32_t>(__ldg(scales + (srow[r][h] + 8 * seg + 1))) << 8;
+        }
+      }
+  };
+  scale_rows(0);
+  const bool resident = TMA && rp.scale_bytes > 0;
+  if (!resident && kw < segs) load_scales(kw);
+  if constexpr (INLINE) {
+    const int pairs = p.T * segs;
+    for (int i0 = warp; i0 < pairs; i0 += 4 * kQ4Warps) {        // four loads in flight
+      uint2 raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = min(i0 + j * kQ4Warps, pairs - 1);
+        raw[j] = q4_fetch(p, i / segs, i % segs);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kQ4Warps;
+        if (i < pairs) q4_operand<AR, TYPE>(raw[j], q4_place(sm_x, i / segs, i % segs, p.T, segs));
+      }
+    }
+    named_bar_sync(1, kQ4Threads);
+  } else if constexpr (!kXRing) {
     pdl_wait();
   }
+  bool ok = true;
+  if (resident) ok = pf_wait_all(&bb.scales, 0, abort, &g_ops_error_q4);
   const float ts = p.tscale ? __ldg(p.tscale) : 1.f;
 
-  for (int b0 = 0; b0 < blocks; b0 += round) {
-    const int b = b0 + team * RB;
-    if (kw < segs) {
-      float acc[RB][NT][4];
+  int it = 0;
+  for (int rd = 0; rd < rounds; ++rd) {
+    float acc[RB][NT][4];
 #pragma unroll
-      for (int r = 0; r < RB; ++r)
+    for (int r = 0; r < RB; ++r)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.f;
-      for (int seg = kw; seg < segs; seg += kw_n) {
-        const size_t tile0 = static_cast<size_t>(seg) * tiles_all + (INLINE ? 0 : (t0 >> 3));
-        const bool same = seg + kw_n < segs;     // the next step is of the same rows
-        const int next = same ? seg + kw_n : kw;
-        if (!same && b0 + round < blocks) rows_of(b + round);
+        for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.f;
+    for (int c = 0; c < chunks; ++c, ++it) {
+      const int slot = it % rp.stages, seg = c * rp.kw + kw;
+      uint4 x[4];
+      float2 fx;
+      auto load_x = [&](int t) {
+        if constexpr (NT == 1) {                 // lanes behind the last token repeat it: their columns are not used
+          const uint8_t* xs = INLINE ? sm_x + seg * p.T * kTokenBytes
+                              : TMA  ? ring + slot * stage + teams * RB * region + kw * p.T * kTokenBytes
+                                     : img + static_cast<size_t>(seg) * p.T * kTokenBytes;
+          const uint8_t* xb = xs + min(g, p.T - 1) * kTokenBytes + 16 * q;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(xb + 64 * i);
+          fx.x = *reinterpret_cast<const float*>(xs + min(2 * q, p.T - 1) * kTokenBytes + 256);
+          fx.y = *reinterpret_cast<const float*>(xs + min(2 * q + 1, p.T - 1) * kTokenBytes + 256);
+        } else {
+          const size_t tile = static_cast<size_t>(seg) * tiles + (t0 >> 3) + t;
+          const uint4* xb = reinterpret_cast<const uint4*>(img + tile * kTileBytes) + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = xb[32 * i];
+          fx = *reinterpret_cast<const float2*>(fac + tile * 8 + 2 * q);
+        }
+      };
+      if constexpr (TMA) ok = ok && pf_wait_all(&bb.full[slot], (it / rp.stages) & 1, abort, &g_ops_error_q4);
+      if (seg < segs && ok) {
+        if constexpr (NT == 1) load_x(0);
+        if (resident) {
+#pragma unroll
+          for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              sc[r][h] = *reinterpret_cast<const uint16_t*>(sm_scales + (srow[r][h] + (kI4 ? 2 * seg : 8 * seg + 2 * q)));
+        }
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-          uint32_t a[2][16];
-          q4_decode<FMT>(f[r], a);
-          const float s0 = FMT == kInt4 ? bf16_bits_to_f32(static_cast<uint16_t>(f[r].s[0])) : 1.f;
-          const float s1 = FMT == kInt4 ? bf16_bits_to_f32(static_cast<uint16_t>(f[r].s[1])) : 1.f;
-          if (same || b0 + round < blocks) q4_load<FMT, WIDE>(p, codes, scales, n[r], next, f[r]);
+          uint4 code[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (TMA) {
+              code[h] = *reinterpret_cast<const uint4*>(ring + slot * stage + r * region + place[h]);
+            } else {
+              const int row = min((first + (rd * teams + team) * RB + r) * R + min(g + 8 * h, R - 1), p.N - 1);
+              const uint8_t* s = p.codes + static_cast<size_t>(row) * (p.K >> 1) + seg * 64 + 16 * q;
+              uint2 a = make_uint2(0, 0), b = a;
+              if (seg * 128 + 32 * q < p.K) a = __ldg(reinterpret_cast<const uint2*>(s));
+              if (seg * 128 + 32 * q + 16 < p.K) b = __ldg(reinterpret_cast<const uint2*>(s + 8));
+              code[h] = make_uint4(a.x, a.y, b.x, b.y);
+            }
+          }
+          AFrag<AR> a;
+          a.decode(code, sc[r]);
+          const float s0 = kI4 ? bf16_bits_to_f32(static_cast<uint16_t>(sc[r][0])) : 1.f;
+          const float s1 = kI4 ? bf16_bits_to_f32(static_cast<uint16_t>(sc[r][1])) : 1.f;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (NT == 1 || t < ntile) {
-              const uint4* xb = reinterpret_cast<const uint4*>(img + (tile0 + t) * kTileBytes) + lane;
-              float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};      // two chains
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint4 x = xb[32 * i];
-                const uint32_t m0[4] = {a[0][4 * i], a[1][4 * i], a[0][4 * i + 1], a[1][4 * i + 1]};
-                const uint32_t m1[4] = {a[0][4 * i + 2], a[1][4 * i + 2], a[0][4 * i + 3], a[1][4 * i + 3]};
-                mma_f16_16816(d, m0, x.x, x.y);
-                mma_f16_16816(e, m1, x.z, x.w);
-              }
-              const float2 fx = *reinterpret_cast<const float2*>(fac + (tile0 + t) * 8 + 2 * q);
-              acc[r][t][0] = fmaf(d[0] + e[0], s0 * fx.x, acc[r][t][0]);
-              acc[r][t][1] = fmaf(d[1] + e[1], s0 * fx.y, acc[r][t][1]);
-              acc[r][t][2] = fmaf(d[2] + e[2], s1 * fx.x, acc[r][t][2]);
-              acc[r][t][3] = fmaf(d[3] + e[3], s1 * fx.y, acc[r][t][3]);
+              if constexpr (NT > 1) load_x(t);
+              float d[4];
+              a.times(x, d);
+              acc[r][t][0] = fmaf(d[0], s0 * fx.x, acc[r][t][0]);
+              acc[r][t][1] = fmaf(d[1], s0 * fx.y, acc[r][t][1]);
+              acc[r][t][2] = fmaf(d[2], s1 * fx.x, acc[r][t][2]);
+              acc[r][t][3] = fmaf(d[3], s1 * fx.y, acc[r][t][3]);
             }
           }
         }
+        if (seg + rp.kw < segs) {
+          if (!resident) load_scales(seg + rp.kw);
+        } else if (rd + 1 < rounds) {
+          scale_rows(rd + 1);
+          if (!resident) load_scales(kw);
+        }
       }
+      if constexpr (TMA) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bb.empty[slot]);
+      }
+    }
+    if (kw < segs) {
 #pragma unroll
       for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           red[((warp * RB + r) * NT + t) * 32 + lane] = make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
     }
-    __syncthreads();
+    if (named_bar_or(team, 32 * rp.kw, !ok)) break;              // a team gives up together
     // add the team's partial sums in warp order
-    const float* rf = reinterpret_cast<const float*>(red);
-    const int parts = min(kw_n, segs);
-    for (int o = threadIdx.x; o < teams * RB * NT * 128; o += kQ4Threads) {
-      const int row = o & 15, tok = (o >> 4) % (8 * NT), r = (o / (128 * NT)) % RB, tm = o / (128 * NT * RB);
-      const int blk = b0 + tm * RB + r, m = block_row(blk) + row;
-      if (t0 + tok >= p.T || m >= block_row(blk + 1)) continue;
-      const int at = (((tm * kw_n * RB + r) * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) * 4 +
-                     (row >> 3) * 2 + (tok & 1);
+    const float* rf = reinterpret_cast<const float*>(red) + team * rp.kw * RB * NT * 128;
+    const int parts = min(rp.kw, segs);
+    for (int o = tid; o < RB * NT * 128; o += 32 * rp.kw) {
+      const int row = o & 15, tok = (o >> 4) % (8 * NT), r = o / (128 * NT);
+      const int n = (first + (rd * teams + team) * RB + r) * R + row;
+      if (t0 + tok >= p.T || row >= R || n >= p.N) continue;
+      const int at = ((r * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) * 4 + (row >> 3) * 2 + (tok & 1);
       float v = 0.f;
+#pragma unroll 4
       for (int w = 0; w < parts; ++w) v += rf[at + w * RB * NT * 128];
-      p.y[static_cast<long long>(t0 + tok) * p.ldy + lo + m] = from_f32<TYPE>(v * ts);
+      p.y[static_cast<long long>(t0 + tok) * p.ldy + n] = from_f32<TYPE>(v * ts);
     }
-    __syncthreads();
+    named_bar_sync(team, 32 * rp.kw);
   }
 }
 
-template <int FMT, int TYPE, int NT, int RB, bool WIDE, bool INLINE>
+template <int AR, int TYPE, int NT, int RB, bool TMA, bool INLINE>
 cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_t s) {
-  const int segs = (p.K + 127) / 128;
-  const int smem = kQ4Warps * RB * NT * 512 + (INLINE ? static_cast<int>(q4_operand_bytes(NT, segs)) : 0);
-  cudaError_t e = allow_smem_once<q4_linear_kernel<FMT, TYPE, NT, RB, WIDE, INLINE>>(dev, 227 * 1024);
+  constexpr int kRed = kQ4Warps * RB * NT * 512, kMost = 226 * 1024 - static_cast<int>(sizeof(RingBars));
+  const int segs = (p.K + 127) / 128, teams = kQ4Warps / kw;
+  RingParams rp;
+  rp.q = p;
+  rp.kw = kw;
+  const int per_cta = (p.N + sms - 1) / sms, round = teams * RB;
+  rp.blocks = ((per_cta + 15) / 16 + round - 1) / round * round;
+  rp.R = (per_cta + rp.blocks - 1) / rp.blocks;
+  constexpr bool kI4 = AR != kExactF16Nvfp4;
+  const long long scale_row = kI4 ? p.K >> 6 : p.K >> 4, scale_all = (rp.blocks * rp.R * scale_row + 127) & ~127ll;
+  const bool sc16 = scale_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0;
+  rp.scale_bytes = TMA && sc16 && scale_all <= kQ4ScaleBytes ? static_cast<int>(scale_all) : 0;
+  const int xstage = TMA && NT == 1 && !INLINE ? kw * p.T * kTokenBytes : 0;
+  const int stage = (teams * RB * ring_region(kw, rp.R) + xstage + 1023) & ~1023;
+  const int rest = kRed + 1024 + rp.scale_bytes + (INLINE ? static_cast<int>(q4_operand_bytes(p.T, segs)) : 0);
+  rp.stages = 0;
+  rp.boxed = p.K % 256 == 0;
+  if constexpr (TMA) {
+    rp.stages = (kMost - rest) / stage;
+    if (rp.stages > kRingMaxStages) rp.stages = kRingMaxStages;
+    if (rp.stages < 1) return cudaErrorInvalidConfiguration;
+    if (!(rp.boxed ? encode_words_blocks(&rp.tm, p.codes, p.N, p.K / 2, rp.R, (kw + 1) / 2)
+                   : encode_words(&rp.tm, p.codes, p.N, p.K / 2, rp.R)))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = allow_smem_once<q4_ring_kernel<AR, TYPE, NT, RB, TMA, INLINE>>(dev, kMost);
   if (e != cudaSuccess) return e;
+  const int total = (p.N + rp.R - 1) / rp.R;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.N < sms ? p.N : sms, (p.T + 8 * NT - 1) / (8 * NT));
-  cfg.blockDim = dim3(kQ4Threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((total + rp.blocks - 1) / rp.blocks, (p.T + 8 * NT - 1) / (8 * NT));
+  cfg.blockDim = dim3(kRingThreads);
+  cfg.dynamicSmemBytes = rp.stages * stage + rest;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = INLINE ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, q4_linear_kernel<FMT, TYPE, NT, RB, WIDE, INLINE>, p, kw);
+  return cudaLaunchKernelEx(&cfg, q4_ring_kernel<AR, TYPE, NT, RB, TMA, INLINE>, rp);
 }
 
-// Blocks of rows at a time: as many as a team has, so that it keeps that many 1 KB loads in flight per warp.
-template <int FMT, int TYPE, int NT, int RBMAX, bool WIDE, bool INLINE>
-cudaError_t launch_q4(const Q4Params& p, int dev, int sms, cudaStream_t s) {
+// Blocks of rows that a team works on at a time: two, sharing a segment's x, where there are as many.
+template <int AR, int TYPE, int NT, bool TMA, bool INLINE>
+cudaError_t launch_ring(const Q4Params& p, int dev, int sms, cudaStream_t s) {
   const int segs = (p.K + 127) / 128;
   int kw = 1;
-  while (kw < segs && kw < kQ4Warps) kw *= 2;
+  while (kw < segs && kw < kQ4Split) kw *= 2;
   const int blocks = ((p.N + sms - 1) / sms + 15) / 16, teams = kQ4Warps / kw;
-  if (blocks <= teams) return launch_rows<FMT, TYPE, NT, 1, WIDE, INLINE>(p, dev, sms, kw, s);
-  if (RBMAX == 2 || blocks <= 2 * teams) return launch_rows<FMT, TYPE, NT, 2, WIDE, INLINE>(p, dev, sms, kw, s);
-  return launch_rows<FMT, TYPE, NT, RBMAX, WIDE, INLINE>(p, dev, sms, kw, s);
+  if (blocks <= teams) return launch_rows<AR, TYPE, NT, 1, TMA, INLINE>(p, dev, sms, kw, s);
+  return launch_rows<AR, TYPE, NT, 2, TMA, INLINE>(p, dev, sms, kw, s);
 }
 
-template <int FMT, int TYPE, bool WIDE>
+template <int AR, int TYPE, bool TMA>
 cudaError_t launch_tokens(const Q4Params& p, cudaStream_t s) {
   int dev, sms;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  const int segs = (p.K + 127) / 128;
-  if (q4_workspace_bytes(p.K, p.T) == 0)
-    return p.T <= 8 ? launch_q4<FMT, TYPE, 1, 4, WIDE, true>(p, dev, sms, s) : launch_q4<FMT, TYPE, 4, 2, WIDE, true>(p, dev, sms, s);
-  const long long pairs = static_cast<long long>(p.T) * segs, ctas = (pairs + 7) / 8;
-  q4_operand_kernel<FMT, TYPE><<<static_cast<int>(ctas < 8 * sms ? ctas : 8 * sms), 256, 0, s>>>(p);
+  if (q4_workspace_bytes(p.K, p.T) == 0) return launch_ring<AR, TYPE, 1, TMA, true>(p, dev, sms, s);
+  const long long pairs = static_cast<long long>(p.T) * ((p.K + 127) / 128), ctas = (pairs + 7) / 8;
+  q4_operand_kernel<AR, TYPE><<<static_cast<int>(ctas < 8 * sms ? ctas : 8 * sms), 256, 0, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.T <= 8) return launch_q4<FMT, TYPE, 1, 4, WIDE, false>(p, dev, sms, s);
-  if (p.T <= 16) return launch_q4<FMT, TYPE, 2, 2, WIDE, false>(p, dev, sms, s);
-  return launch_q4<FMT, TYPE, 4, 2, WIDE, false>(p, dev, sms, s);
+  if (p.T <= 8) return launch_ring<AR, TYPE, 1, TMA, false>(p, dev, sms, s);
+  if (p.T <= 16) return launch_ring<AR, TYPE, 2, TMA, false>(p, dev, sms, s);
+  return launch_ring<AR, TYPE, 4, TMA, false>(p, dev, sms, s);
 }
 
-template <int FMT, bool WIDE>
+template <int AR, bool TMA>
 cudaError_t launch_type(const Q4Params& p, cudaStream_t s) {
-  return p.type == kTBf16 ? launch_tokens<FMT, kTBf16, WIDE>(p, s) : launch_tokens<FMT, kTF16, WIDE>(p, s);
+  return p.type == kTBf16 ? launch_tokens<AR, kTBf16, TMA>(p, s) : launch_tokens<AR, kTF16, TMA>(p, s);
 }
 
 }  // namespace
 
+cudaError_t read_q4_error(unsigned* out) {
+  const unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_ops_error_q4, sizeof(unsigned));
+  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_ops_error_q4, &zero, sizeof(unsigned));
+  return e;
+}
+
 size_t q4_workspace_bytes(int K, int T) {
   const int segs = (K + 127) / 128;
-  if (T <= 32 && T * segs <= kQ4Inline && q4_operand_bytes(T <= 8 ? 1 : 4, segs) <= kQ4InlineBytes) return 0;
-  return q4_operand_bytes((T + 7) / 8, segs);
+  if (T <= 8 && segs <= kQ4Inline) return 0;
+  return q4_operand_bytes(T, segs);
 }
 
 cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s) {
-  if (p.fmt == kInt4) return launch_type<kInt4, true>(p, s);
-  // 16-byte rows of codes and 2-byte aligned scales where the widths and the pointers allow
-  const bool wide = p.K % 32 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 1u) == 0;
-  return wide ? launch_type<kNvfp4, true>(p, s) : launch_type<kNvfp4, false>(p, s);
+  if (p.fmt == kInt4) return p.rotated ? launch_type<kLimbs, true>(p, s) : launch_type<kExactF16Int4, true>(p, s);
+  // 16-byte rows of codes and 2-byte aligned pairs of scales where the width and the pointer allow
+  const bool tma = p.K % 32 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 1u) == 0;
+  return tma ? launch_type<kExactF16Nvfp4, true>(p, s) : launch_type<kExactF16Nvfp4, false>(p, s);
 }
 
 }  // namespace flint
