@@ -9,7 +9,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflint_moe.so")
 SOURCES = ["api.cu", "route.cu", "decode.cu", "prefill.cu", "stack.cu", "noalloc.cu", "quant.cu", "w4a4.cu",
-           "q4_linear.cu", "grouped.cu", "experts.cu", "norm.cu", "ops_api.cu"]
+           "q4_linear.cu", "q4_mma.cu", "grouped.cu", "experts.cu", "norm.cu", "ops_api.cu"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr"]
 

@@ -23,6 +23,7 @@ struct Q4Params {
 };
 size_t q4_workspace_bytes(int K, int T);
 cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s);
+cudaError_t launch_q4_mma(const Q4Params& p, cudaStream_t s);         // T > 8, rows of codes in whole 16 bytes
 
 struct GroupedParams {
   int E, N, K, act, type;
@@ -40,6 +41,7 @@ struct GroupedParams {
 cudaError_t launch_grouped_linear(const GroupedParams& p, cudaStream_t s);
 cudaError_t read_ops_error(unsigned* out);       // of the current device; waits for it, clears the words
 cudaError_t read_q4_error(unsigned* out);
+cudaError_t read_q4_mma_error(unsigned* out);
 
 cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, int* perm, int* inv, cudaStream_t s);
 

@@ -1,27 +1,17 @@
 // Linear products with 4-bit weights for few tokens (flint_q4_linear):
 //   y[t][n] = ts * sum over 128-segments of  s[n] * (code[n] . x'[t]),  x' = x or blockdiag(Hn) x.
 //
-// Bound by streaming the weights once, and close behind it by the instructions that decode them. The rows of W are
-// divided evenly over one CTA per SM (not in units of a tile); 16 warps split K: a warp takes a 128-segment of up to RB
-// blocks of up to 16 rows at a time, as fragments of mma.sync. A fragment's K order is free as long as x has the same:
-// a lane's 16 bytes are 32 neighbouring K of one row.
-//
-// How codes meet x, per 128-segment (Arith):
-//   kExactF16  int4 without rotation, NVFP4: codes become exact fp16 (int4: -8..7; NVFP4: E2M1 x E4M3, six significant
-//              bits); x is fp16 after one power of two per (token, segment) that brings the segment's largest finite
-//              value into [2^14, 2^15): 16-bit inputs stay exact down to 2^-29 of it (2^-38 absolute). The factor is
-//              taken out of the fp32 sum again, so no range is lost for either type.
-//   kLimbs     rotated int4: Hn x is rounded to 16-bit fixed point per (token, segment), a unit being 2^-14 of the power
-//              of two below the segment's largest value (rotation spreads outliers, so that is finer than fp16 for all
-//              but the smallest values); its signed high and unsigned low bytes multiply the exact int8 16 c on the
-//              integer tensor cores. Three instructions decode eight codes instead of nine (8192 x 8192, T = 8: see
-//              launch_ring).
-// The int4 group scale multiplies the segment's sum in fp32.
+// Up to 8 tokens (this file; more: q4_mma.cu) it is bound by streaming the weights once, and close behind by the
+// instructions that decode them. The rows of W are divided evenly over one CTA per SM (not in units of a tile); the 16
+// warps of a CTA split K: a warp takes a 128-segment of one or two blocks of up to 16 rows at a time, as fragments of
+// mma.sync. A fragment's K order is free as long as x has the same: a lane's 16 bytes are 32 neighbouring K of one row.
+// The int4 group scale and the operand's factor (q4_operand.cuh) multiply the segment's sum in fp32.
 //
 // With few segments every CTA builds the operand itself in shared memory; with more, one kernel builds it once in the
 // workspace and the product kernel, launched behind it as a programmatic dependent, starts its weight copies meanwhile.
 #include "kernels.cuh"
 #include "ops.cuh"
+#include "q4_operand.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
 
@@ -33,141 +23,10 @@ namespace {
 
 constexpr int kQ4Threads = 512;
 constexpr int kQ4Warps = kQ4Threads / 32;
-// Segments up to which each CTA builds the operand of up to 8 tokens itself (at most 8 pairs per warp and 33 KB)
-constexpr int kQ4Inline = 16;
-
-enum Arith : int { kExactF16Int4, kExactF16Nvfp4, kLimbs };
-
-// The operand of one (token, segment): four chunks of 16 bytes for each of the four lanes q that read it, K = 32 q ..
-// 32 q + 31. fp16: chunk i holds K = 32 q + 8 i .. + 7 in the order of the decoded pairs; limbs: chunk 2 limb + (i >> 1)
-// holds at 8 (i & 1) the bytes of K = 32 q + 8 i + 0, 2, 4, 6 and of + 1, 3, 5, 7.
-// Up to 8 tokens (the ring kernel copies what is there): [segment][token][chunk][q], then the inverse factor, kTokenBytes
-// each. More tokens: [segment][tile of 8][chunk][token][q], so that a warp's loads are contiguous, and behind all of
-// them the factors [segment][tile][8].
-constexpr int kTokenBytes = 272;
-constexpr int kTileBytes = 2048;
-
-__host__ __device__ inline size_t q4_operand_bytes(int T, int segs) {
-  return T <= 8 ? static_cast<size_t>(T) * segs * kTokenBytes : static_cast<size_t>((T + 7) / 8) * segs * (kTileBytes + 32);
-}
-
-struct OperandPlace {
-  uint8_t* at;                                   // of chunk 0, q = 0
-  int chunk;                                     // bytes from a chunk to the next
-  float* factor;
-};
-
-__device__ __forceinline__ OperandPlace q4_place(uint8_t* img, int t, int seg, int T, int segs) {
-  OperandPlace o;
-  if (T <= 8) {
-    o.at = img + (static_cast<size_t>(seg) * T + t) * kTokenBytes;
-    o.chunk = 64;
-    o.factor = reinterpret_cast<float*>(o.at + 256);
-  } else {
-    const size_t tiles = (T + 7) / 8, tile = seg * tiles + (t >> 3);
-    o.at = img + tile * kTileBytes + (t & 7) * 64;
-    o.chunk = 512;
-    o.factor = reinterpret_cast<float*>(img + tiles * segs * kTileBytes) + tile * 8 + (t & 7);
-  }
-  return o;
-}
-
-// A warp's four elements per lane of one (token, segment).
-__device__ __forceinline__ uint2 q4_fetch(const Q4Params& p, int t, int seg) {
-  const int k = seg * 128 + 4 * (threadIdx.x & 31);
-  // K is a multiple of 16: four neighbours are in or out together
-  return k < p.K ? __ldg(reinterpret_cast<const uint2*>(p.x + t * p.ldx + k)) : make_uint2(0, 0);
-}
-
-// The operand of one (token, segment) by one warp.
-template <int AR, int TYPE>
-__device__ __forceinline__ void q4_operand(const uint2& raw, const OperandPlace& o) {
-  const int lane = threadIdx.x & 31;
-  const float2 v01 = pair_to_f32<TYPE>(raw.x), v23 = pair_to_f32<TYPE>(raw.y);
-  float v[4] = {v01.x, v01.y, v23.x, v23.y};
-  if constexpr (AR == kLimbs) fwht128_warp(v);
-  uint32_t m = 0;
-  bool odd_ones = false;                         // infinities or NaN
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    if (a < 0x7F800000u) m = max(m, a);
-    else odd_ones = true;
-  }
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
-  const int e = min(max(static_cast<int>(m >> 23), 15), 254);      // biased exponent of the largest value
-  const float f = m ? __uint_as_float(static_cast<uint32_t>(268 - e) << 23) : 1.f;     // 2^(141 - e)
-  float inv = m ? __uint_as_float(static_cast<uint32_t>(e - 14) << 23) : 1.f;
-  uint8_t* at = o.at + (lane >> 3) * 16;
-  const int i = (lane >> 1) & 3;
-  const bool odd = lane & 1;
-  uint2 u;
-  if constexpr (AR == kLimbs) {
-    uint32_t hi = 0, lo = 0;                     // bytes 0, 1: elements 0, 2; bytes 2, 3: elements 1, 3
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = min(__float2int_rn(v[j] * f), 32767);
-      const int sh = 8 * ((j >> 1) + 2 * (j & 1));
-      hi |= (static_cast<uint32_t>(n >> 8) & 0xFFu) << sh;
-      lo |= (static_cast<uint32_t>(n) & 0xFFu) << sh;
-    }
-    // the even lane of a pair writes the high limbs of the eight, the odd lane the low ones
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? hi : lo, 1);
-    const uint32_t first = odd ? got : hi, second = odd ? lo : got;
-    u = make_uint2(__byte_perm(first, second, 0x5410), __byte_perm(first, second, 0x7632));
-    at += (2 * odd + (i >> 1)) * o.chunk + (i & 1) * 8;
-    inv *= 0.0625f;                              // the codes enter as 16 c
-    // what is infinite or no number stays so, for the token's whole sum
-    if (__any_sync(0xFFFFFFFFu, odd_ones)) inv = __uint_as_float(0x7FC00000u);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= f;       // infinities and NaN pass through as they are
-    if constexpr (AR == kExactF16Int4) {         // 8-block order 0,4,1,5,2,6,3,7: see int4x8_to_half2x4
-      const float r0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[2], 1);
-      const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[1] : v[3], 1);
-      u = odd ? make_uint2(pack_half2(r0, v[2]), pack_half2(r1, v[3])) : make_uint2(pack_half2(v[0], r0), pack_half2(v[1], r1));
-    } else {
-      u = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
-    }
-    at += i * o.chunk + 8 * odd;
-  }
-  *reinterpret_cast<uint2*>(at) = u;
-  if (lane == 0) *o.factor = inv;
-}
-
-template <int AR, int TYPE>
-__global__ void __launch_bounds__(256) q4_operand_kernel(const __grid_constant__ Q4Params p) {
-  pdl_trigger();                                 // the product kernel waits for this one before it reads the operand
-  const int segs = (p.K + 127) / 128;
-  for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < static_cast<long long>(p.T) * segs;
-       i += static_cast<long long>(gridDim.x) * 8) {
-    const int t = static_cast<int>(i / segs), seg = static_cast<int>(i - static_cast<long long>(t) * segs);
-    q4_operand<AR, TYPE>(q4_fetch(p, t, seg), q4_place(static_cast<uint8_t*>(p.workspace), t, seg, p.T, segs));
-  }
-}
-
-// ---------------------------------------------------------------------------------------------
-// fragments
-
-// One row's 32 codes (16 bytes) as fp16 pairs, the order of the fp16 operand; s2: the two block scales (NVFP4).
-template <int AR>
-__device__ __forceinline__ void decode_f16(const uint4& c, uint32_t s2, uint32_t (&d)[16]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (AR == kExactF16Int4) {
-      uint32_t pr[4];
-      int4x8_to_half2x4(w[i], pr);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[4 * i + j] = pr[j];
-    } else {
-      const uint32_t h = e4m3_to_half_bits((s2 >> (8 * (i >> 1))) & 0xFFu);
-      const uint32_t hh = h | (h << 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[4 * i + j] = hmul2_u32(e2m1x2_to_half2(w[i] >> (8 * j)), hh);
-    }
-  }
-}
+// (token, segment) pairs up to which each CTA builds the operand itself: 8 per warp would take 5 us, the separate kernel
+// puts off the first product by 2.5 us.
+constexpr int kQ4Inline = 64;
+constexpr int kQ4InlineBytes = 40 * 1024;
 
 // d += A B on the integer tensor cores (m16n8k32): A s8, B s8 or u8
 template <bool SIGNED_B>
@@ -282,7 +141,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
   const int xstage = kXRing ? rp.kw * p.T * kTokenBytes : 0;
   const int stage = (teams * RB * region + xstage + 1023) & ~1023;
   const int total = (p.N + R - 1) / R, first = blockIdx.x * rp.blocks, rounds = rp.blocks / (teams * RB);
-  constexpr bool kI4 = AR != kExactF16Nvfp4;
+  constexpr bool kI4 = AR != kF16Nvfp4;
   const size_t scale_row = kI4 ? p.K >> 6 : p.K >> 4;            // bytes
   uint8_t* ring = align1024(smem_raw);
   float4* red = reinterpret_cast<float4*>(ring + rp.stages * stage);           // [warps][RB][NT][32]
@@ -399,18 +258,17 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
   if (!resident && kw < segs) load_scales(kw);
   if constexpr (INLINE) {
     const int pairs = p.T * segs;
-    for (int i0 = warp; i0 < pairs; i0 += 4 * kQ4Warps) {        // four loads in flight
+    for (int i0 = warp; i0 < pairs; i0 += 4 * kQ4Warps) {
       uint2 raw[4];
+      OperandPlace o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = min(i0 + j * kQ4Warps, pairs - 1);
-        raw[j] = q4_fetch(p, i / segs, i % segs);
+        const int i = min(i0 + j * kQ4Warps, pairs - 1), t = i / segs, seg = i - t * segs;
+        raw[j] = q4_fetch(p, t, seg);
+        o[j] = q4_place<kTokens>(sm_x, t, seg, p.T, segs);
+        if (i0 + j * kQ4Warps >= pairs) o[j].at = nullptr;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * kQ4Warps;
-        if (i < pairs) q4_operand<AR, TYPE>(raw[j], q4_place(sm_x, i / segs, i % segs, p.T, segs));
-      }
+      q4_operand<AR, TYPE, 4>(raw, p.rotated != 0, o);
     }
     named_bar_sync(1, kQ4Threads);
   } else if constexpr (!kXRing) {
@@ -541,7 +399,7 @@ cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_
   const int per_cta = (p.N + sms - 1) / sms, round = teams * RB;
   rp.blocks = ((per_cta + 15) / 16 + round - 1) / round * round;
   rp.R = (per_cta + rp.blocks - 1) / rp.blocks;
-  constexpr bool kI4 = AR != kExactF16Nvfp4;
+  constexpr bool kI4 = AR != kF16Nvfp4;
   const long long scale_row = kI4 ? p.K >> 6 : p.K >> 4, scale_all = (rp.blocks * rp.R * scale_row + 127) & ~127ll;
   const bool sc16 = scale_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0;
   rp.scale_bytes = TMA && sc16 && scale_all <= kQ4ScaleBytes ? static_cast<int>(scale_all) : 0;
@@ -591,12 +449,16 @@ cudaError_t launch_tokens(const Q4Params& p, cudaStream_t s) {
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   if (q4_workspace_bytes(p.K, p.T) == 0) return launch_ring<AR, TYPE, 1, TMA, true>(p, dev, sms, s);
-  const long long pairs = static_cast<long long>(p.T) * ((p.K + 127) / 128), ctas = (pairs + 7) / 8;
-  q4_operand_kernel<AR, TYPE><<<static_cast<int>(ctas < 8 * sms ? ctas : 8 * sms), 256, 0, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.T <= 8) return launch_ring<AR, TYPE, 1, TMA, false>(p, dev, sms, s);
-  if (p.T <= 16) return launch_ring<AR, TYPE, 2, TMA, false>(p, dev, sms, s);
-  return launch_ring<AR, TYPE, 4, TMA, false>(p, dev, sms, s);
+  if (p.T <= 8) {
+    if ((e = launch_q4_operand<AR, TYPE, kTokens>(p, sms, s)) != cudaSuccess) return e;
+    return launch_ring<AR, TYPE, 1, TMA, false>(p, dev, sms, s);
+  }
+  if constexpr (TMA) {
+    return launch_q4_mma(p, s);
+  } else {
+    if ((e = launch_q4_operand<AR, TYPE, kTiles>(p, sms, s)) != cudaSuccess) return e;
+    return launch_ring<AR, TYPE, 4, TMA, false>(p, dev, sms, s);
+  }
 }
 
 template <int AR, bool TMA>
@@ -610,20 +472,23 @@ cudaError_t read_q4_error(unsigned* out) {
   const unsigned zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(out, g_ops_error_q4, sizeof(unsigned));
   if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_ops_error_q4, &zero, sizeof(unsigned));
+  unsigned more = 0;
+  if (e == cudaSuccess) e = read_q4_mma_error(&more);
+  *out |= more;
   return e;
 }
 
 size_t q4_workspace_bytes(int K, int T) {
   const int segs = (K + 127) / 128;
-  if (T <= 8 && segs <= kQ4Inline) return 0;
+  if (T <= 8 && T * segs <= kQ4Inline && q4_operand_bytes(T, segs) <= kQ4InlineBytes) return 0;
   return q4_operand_bytes(T, segs);
 }
 
 cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s) {
-  if (p.fmt == kInt4) return p.rotated ? launch_type<kLimbs, true>(p, s) : launch_type<kExactF16Int4, true>(p, s);
+  if (p.fmt == kInt4) return p.rotated ? launch_type<kLimbs, true>(p, s) : launch_type<kF16Int4, true>(p, s);
   // 16-byte rows of codes and 2-byte aligned pairs of scales where the width and the pointer allow
   const bool tma = p.K % 32 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 1u) == 0;
-  return tma ? launch_type<kExactF16Nvfp4, true>(p, s) : launch_type<kExactF16Nvfp4, false>(p, s);
+  return tma ? launch_type<kF16Nvfp4, true>(p, s) : launch_type<kF16Nvfp4, false>(p, s);
 }
 
 }  // namespace flint
