@@ -75,6 +75,14 @@ struct NormParams {
 };
 cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s);
 
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_3d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
                                             uint64_t pol) {
   asm volatile(
