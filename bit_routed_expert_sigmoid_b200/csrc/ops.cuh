@@ -23,7 +23,7 @@ struct Q4Params {
 };
 size_t q4_workspace_bytes(int K, int T);
 cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s);
-cudaError_t launch_q4_mma(const Q4Params& p, cudaStream_t s);         // T > 8, rows of codes in whole 16 bytes
+cudaError_t launch_q4_mma(const Q4Params& p, cudaStream_t s);         // T > 8
 
 struct GroupedParams {
   int E, N, K, act, type;
@@ -90,6 +90,17 @@ __device__ __forceinline__ void tma_3d_hint(void* dst, const CUtensorMap* map, i
       "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(pol)
       : "memory");
+}
+
+// Barrier over the CTAs of the cluster (all threads of each), ordering shared-memory accesses, remote ones too.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores to the same place of CTA `rank`'s shared memory.
+__device__ __forceinline__ void st_cluster_f32(float* p, int rank, float v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 // 16-bit element of an activation tensor as fp32, and back (one rounding, to nearest even)

@@ -453,12 +453,7 @@ cudaError_t launch_tokens(const Q4Params& p, cudaStream_t s) {
     if ((e = launch_q4_operand<AR, TYPE, kTokens>(p, sms, s)) != cudaSuccess) return e;
     return launch_ring<AR, TYPE, 1, TMA, false>(p, dev, sms, s);
   }
-  if constexpr (TMA) {
-    return launch_q4_mma(p, s);
-  } else {
-    if ((e = launch_q4_operand<AR, TYPE, kTiles>(p, sms, s)) != cudaSuccess) return e;
-    return launch_ring<AR, TYPE, 4, TMA, false>(p, dev, sms, s);
-  }
+  return launch_q4_mma(p, s);
 }
 
 template <int AR, bool TMA>
