@@ -109,7 +109,7 @@ struct AFrag<kLimbs> {
 constexpr int kRingThreads = kQ4Threads + 32;
 constexpr int kRingMaxStages = 8;
 constexpr int kQ4Split = 8;                      // warps of a team: two teams of 8 use a stage's x twice
-constexpr int kQ4ScaleBytes = 48 * 1024;         // scales kept in shared memory at most
+constexpr int kQ4ScaleBytes = 72 * 1024;         // scales kept in shared memory at most
 
 struct RingParams {
   CUtensorMap tm;                                // boxed: [K / 256][N][128 bytes], else [N][K / 2 bytes]

@@ -2,7 +2,8 @@
 //
 // The weights are the M side of the MMA, decoded straight into tensor memory: a tile is up to 128 rows of W, and a
 // cluster of CTAs splits a tile's K, so that tiles of equal height and K ranges fill the SMs whatever N is (8192 rows: 74
-// tiles of 111 rows, two CTAs each). Two teams of four warps take 128-segments in turn, a thread decoding one row's 128
+// tiles of 111 rows, two CTAs each). Four teams of four warps take 128-segments in turn (two: 23 us for 8192 x 8192 at
+// T = 16), a thread decoding one row's 128
 // codes to exact fp16; two warps issue the MMAs of a segment in turn (an instruction takes ~45 cycles to issue), each
 // into an accumulator of the segment's own; eight warps add the accumulators, times the rows' group scales and the
 // tokens' factors, to fp32 sums in registers: scales of any range and tokens of any magnitude lose nothing. At the end
@@ -23,7 +24,9 @@ __device__ unsigned g_ops_error_q4mma;           // timeout bits of bounded wait
 
 namespace {
 
-constexpr int kMmThreads = 640;                  // copies: 2 warps, MMA: 2, decoding: 2 x 4, sums: 8
+constexpr int kMmTeams = 4;                      // decoding teams of four warps
+constexpr int kMmSums = 4 + 4 * kMmTeams;        // first of the 8 summing warps; before: copies 2, MMA 2, decoding
+constexpr int kMmThreads = 32 * (kMmSums + 8);
 constexpr int kMmTokens = 64;                    // tokens at a time at most
 constexpr int kMmChunk = 4;                      // segments of codes per stage
 constexpr int kMmA = 4;                          // decoded segments in tensor memory (64 columns each)
@@ -69,6 +72,15 @@ __device__ __forceinline__ void add_scaled(float& a0, float& a1, uint32_t d0, ui
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
+// 16 consecutive columns of the warp's 32 lanes
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
 template <int AR, int TYPE, bool TMA>
 __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_constant__ MmParams mp) {
   const Q4Params& p = mp.q;
@@ -94,7 +106,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMmMaxStages; ++i) {
       mbar_init(&bb.c_full[i], 1);
-      mbar_init(&bb.c_empty[i], 8);
+      mbar_init(&bb.c_empty[i], 4 * kMmTeams);
       mbar_init(&bb.b_full[i], 1);
       mbar_init(&bb.b_empty[i], 2);
     }
@@ -120,7 +132,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bb.tmem, tmem_a = tmem + kMmD * 64;
-  const int half = (warp - 12) >> 2;             // sums: which 16 of every 32 tokens
+  const int half = (warp - kMmSums) >> 2;             // sums: which 16 of every 32 tokens
   float acc[kMmTokens / 2];                      // sums: tokens 16 (2 b + half) + j at 16 b + j
 #pragma unroll
   for (int j = 0; j < kMmTokens / 2; ++j) acc[j] = 0.f;
@@ -193,8 +205,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     }
     tc_commit_w(&bb.done[w]);
     pf_wait_all(&bb.done[w], 0, abort, err);
-  } else if (warp < 12) {
-    // ---- decoding: a thread per row, 128 codes of every second segment
+  } else if (warp < kMmSums) {
+    // ---- decoding: a thread per row, 128 codes of every fourth segment
     const int team = (warp - 4) >> 2, row = 32 * (warp & 3) + lane;
     const int n = min(row0 + min(row, R - 1), p.N - 1);
     const uint32_t lane_base = tmem_a + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -202,7 +214,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     for (int c = 0; c < chunks && ok; ++c) {
       const int sc = c % mp.SC;
       if (TMA && !(ok = pf_wait_all(&bb.c_full[sc], (c / mp.SC) & 1, abort, err))) break;
-      for (int j = team; j < kMmChunk; j += 2) {
+      for (int j = team; j < kMmChunk; j += kMmTeams) {
         const int seg = c * kMmChunk + j, sa = seg % kMmA;
         if (seg >= segs) break;
         uint2 scale = make_uint2(0, 0);          // NVFP4: the eight block scales
@@ -235,16 +247,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
           for (int i = 0; i < 4; ++i) code[i] = make_uint4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {            // 64 codes: 32 columns
-          uint32_t v[32];
-          const uint32_t s2 = h ? scale.y : scale.x;
-          decode_f16<AR>(code[2 * h], s2 & 0xFFFFu, *reinterpret_cast<uint32_t(*)[16]>(v));
-          decode_f16<AR>(code[2 * h + 1], s2 >> 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
-          if (h == 0) {
+        for (int i = 0; i < 4; ++i) {            // 32 codes: 16 columns
+          uint32_t v[16];
+          const uint32_t s2 = i < 2 ? scale.x : scale.y;
+          decode_f16<AR>(code[i], i & 1 ? s2 >> 16 : s2 & 0xFFFFu, v);
+          if (i == 0) {
             if (seg >= kMmA && !(ok = pf_wait_all(&bb.a_empty[sa], ((seg / kMmA) - 1) & 1, abort, err))) break;
             tc_fence_after();
           }
-          tc_st32(lane_base + sa * 64 + h * 32, v);
+          tc_st16(lane_base + sa * 64 + i * 16, v);
         }
         if (!ok) break;
         tc_wait_st();
@@ -274,34 +285,32 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
       }
       if (!(ok = pf_wait_all(&bb.d_full[sd], (seg / kMmD) & 1, abort, err))) break;
       tc_fence_after();
-      uint32_t d[2][16];
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        if (16 * (2 * b + half) < N16) tc_ld16(base + sd * 64 + 16 * (2 * b + half), d[b]);
-      tc_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bb.d_empty[sd]);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int c0 = 16 * (2 * b + half);
         if (c0 < N16) {
+          uint32_t d[16];
+          tc_ld16(base + sd * 64 + c0, d);
+          tc_wait_ld();
           const float* f = &s_factor[seg % kMmRing][c0];
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const float4 v = *reinterpret_cast<const float4*>(f + i);
-            add_scaled(acc[16 * b + i], acc[16 * b + i + 1], d[b][i], d[b][i + 1], sc, v.x, v.y);
-            add_scaled(acc[16 * b + i + 2], acc[16 * b + i + 3], d[b][i + 2], d[b][i + 3], sc, v.z, v.w);
+            add_scaled(acc[16 * b + i], acc[16 * b + i + 1], d[i], d[i + 1], sc, v.x, v.y);
+            add_scaled(acc[16 * b + i + 2], acc[16 * b + i + 3], d[i + 2], d[i + 3], sc, v.z, v.w);
           }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.d_empty[sd]);
     }
 #pragma unroll
     for (int j = 0; j < kMmTokens / 2; ++j) acc[j] *= ts;
   }
 
   // ---- the CTAs of a tile add their sums: CTA r finishes the tokens of its share
-  const bool summing = warp >= 12;
+  const bool summing = warp >= kMmSums;
   const int row = 32 * (warp & 3) + lane;
   if (mp.split == 1) {
     if (summing && row < rows) {
@@ -318,19 +327,32 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     cluster_sync();                              // every CTA is done with its rings
     if (summing) {
 #pragma unroll
-      for (int j = 0; j < kMmTokens / 2; ++j) {
-        const int t = 16 * (2 * (j >> 4) + half) + (j & 15);
-        if (t < TB) st_cluster_f32(part + (rank * share + t % share) * 128 + row, t / share, acc[j]);
+      for (int b = 0; b < 2; ++b) {
+        int t = 16 * (2 * b + half), to = t / share, at = t - to * share;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, ++t) {
+          if (t < TB) st_cluster_f32(part + (rank * share + at) * 128 + row, to, acc[16 * b + j]);
+          if (++at == share) at = 0, ++to;
+        }
       }
     }
     __syncwarp();
     cluster_sync();
-    for (int i = threadIdx.x; i < share * 128; i += kMmThreads) {
-      const int r = i & 127, t = rank * share + (i >> 7);
-      if (r >= rows || t >= TB || t0 + t >= p.T) continue;
-      float v = 0.f;
-      for (int k = 0; k < mp.split; ++k) v += part[(k * share + (i >> 7)) * 128 + r];
-      p.y[static_cast<long long>(t0 + t) * p.ldy + row0 + r] = from_f32<TYPE>(v);
+    // a warp per token, four rows per lane
+    for (int i = warp; i < share; i += kMmThreads / 32) {
+      const int t = rank * share + i;
+      if (t >= TB || t0 + t >= p.T) break;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < mp.split; ++k) {
+        const float4 u = *reinterpret_cast<const float4*>(part + (k * share + i) * 128 + 4 * lane);
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
+      uint16_t* y = p.y + static_cast<long long>(t0 + t) * p.ldy + row0 + 4 * lane;
+      const int left = rows - 4 * lane;
+      if (left > 0) y[0] = from_f32<TYPE>(v.x);
+      if (left > 1) y[1] = from_f32<TYPE>(v.y);
+      if (left > 2) y[2] = from_f32<TYPE>(v.z);
+      if (left > 3) y[3] = from_f32<TYPE>(v.w);
     }
   }
 
@@ -394,7 +416,8 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
       mp.R = R < 8 ? 8 : R;
     }
   }
-  mp.range = ((segs + mp.split - 1) / mp.split + 1) & ~1;        // even: 256-code blocks and pairs start with the range
+  mp.range = (segs + mp.split - 1) / mp.split;
+  if (TMA) mp.range = (mp.range + 1) & ~1;       // a range starts with a 256-code block
   const int tiles = (p.N + mp.R - 1) / mp.R;
   const int token_chunks = (p.T + kMmTokens - 1) / kMmTokens;
   mp.TB = ((p.T + token_chunks - 1) / token_chunks + 7) & ~7;
