@@ -48,7 +48,7 @@ struct GrGeom {
   static constexpr int kB = NMAX * 128;          // a stage of rows: NMAX rows x 64 K
   static constexpr int kStage = kGrABytes + kB;
   static constexpr int kStages = 192 * 1024 / kStage;      // 8 (64), 6 (128), 4 (256)
-  static constexpr int kBox = NMAX == 64 ? 16 : 32;        // rows of a TMA box of x
+  static constexpr int kBox = NMAX == 256 ? 128 : 64;      // rows of a TMA box of x
 };
 
 struct GrTab {
@@ -102,12 +102,12 @@ __device__ __forceinline__ GrTile gr_tile(const GrTab& tt, int E, int t) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives at `bar` (one of the arrivals it was made for) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Makes this thread's shared-memory writes visible to the tensor core's reads (async proxy).
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Orders shared-memory writes that this thread has observed (or made) before its later tensor-core reads of them.
 __device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Waits until the copies of iterations [max(it - stages, 0), it) have landed, so that none is in flight when the
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(&bb.full[i], GATHER ? 1 + kGrGather / 32 : 2);
+      mbar_init(&bb.full[i], GATHER ? 1 + kGrGather : 2);
       mbar_init(&bb.empty[i], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -241,23 +241,19 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
       drain_copies(bb.full, G::kStages, it);
     }
   } else if (GATHER && warp >= kGrThreads / 32) {
-    // eight lanes per row of 128 bytes; a stage is handed over kLag stages after its copies were issued
-    constexpr int kLag = G::kStages / 2, kPass = NMAX / 16;
+    // eight lanes per row of 128 bytes; a stage's barrier completes when every thread's copies have landed
+    constexpr int kPass = NMAX / 16;
     const int tid = threadIdx.x - kGrThreads, c = tid & 7, r0 = tid >> 3;
     const uint32_t dst0 = smem_u32(sm) + kGrABytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
     int it = 0;
     bool ok = true;
-    auto hand_over = [&](int j) {
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bb.full[j % G::kStages]);
-    };
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
       const int passes = (tl.n + 15) >> 4;                   // rows behind the last one repeat it: unused columns
-      int src[kPass];
+      const uint16_t* src[kPass];
 #pragma unroll
-      for (int i = 0; i < kPass; ++i) src[i] = i < passes ? source_row(p, tl.row0 + min(r0 + 16 * i, tl.n - 1)) : 0;
+      for (int i = 0; i < kPass; ++i)
+        src[i] = p.x + (i < passes ? source_row(p, tl.row0 + min(r0 + 16 * i, tl.n - 1)) * p.ldx : 0);
       for (int s = 0; s < steps; ++s, ++it) {
         const int slot = it % G::kStages;
         if (it >= G::kStages && !pf_wait_all(&bb.empty[slot], ((it / G::kStages) - 1) & 1, abort, &g_ops_error)) {
@@ -266,20 +262,14 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
         }
         const int k = s * 64 + 8 * c;
         const bool in = k < p.K;
-        const uint16_t* x = p.x + (in ? k : 0);
         const uint32_t dst = dst0 + slot * G::kStage;
 #pragma unroll
         for (int i = 0; i < kPass; ++i)
-          if (i < passes) cp_async16(dst + i * 2048, x + src[i] * p.ldx, in);
-        cp_async_commit();
-        if (it >= kLag) {
-          cp_async_wait<kLag>();
-          hand_over(it - kLag);
-        }
+          if (i < passes) cp_async16(dst + i * 2048, src[i] + (in ? k : 0), in);
+        cp_async_arrive(&bb.full[slot]);
       }
     }
-    cp_async_wait<0>();
-    for (int j = max(it - kLag, 0); j < it; ++j) hand_over(j);
+    cp_async_wait_all();
   } else if (warp == 1) {
     int it = 0, ti = 0;
     bool ok = true;
@@ -296,6 +286,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
           ok = false;
           break;
         }
+        if constexpr (GATHER) fence_proxy_async_shared();     // the rows were written by ordinary (cp.async) copies
         tc_fence_after();
         const uint32_t a0 = smem_u32(sm + slot * G::kStage), b0 = a0 + kGrABytes;
 #pragma unroll
@@ -336,7 +327,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const float o = from[c * 64], v = __uint_as_float(own[c]);
-            const float h = up ? silu(o) * v : silu(v) * o;
+            const float h = up ? silu_fast(o) * v : silu_fast(v) * o;
             if (j0 + 16 * up + c < tl.n && n < nout) yr[c * p.ldy] = from_f32<TYPE>(h);
           }
         }
@@ -589,7 +580,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
           r0 += rf[at4 + w * NT * 128 + (ACT ? 0 : (j >> 3) * 2)];
           if constexpr (ACT) r1 += rf[at4 + w * NT * 128 + 2];
         }
-        p.y[static_cast<long long>(off + tok) * p.ldy + nn] = from_f32<TYPE>(ACT ? silu(r0) * r1 : r0);
+        p.y[static_cast<long long>(off + tok) * p.ldy + nn] = from_f32<TYPE>(ACT ? silu_fast(r0) * r1 : r0);
       }
     named_bar_sync(team, 32 * ge.kw);
     un += teams;
