@@ -20,10 +20,11 @@ __device__ unsigned g_ops_error;                 // timeout bits of bounded wait
 namespace {
 
 constexpr int kGrMaxE = 1024;
-constexpr int kGrThreads = 256;                  // 8 warps, and 4 more that gather rows
+constexpr int kGrThreads = 384;                  // copies: 2 warps, MMA: 1, idle: 1, epilogue: 8; and 4 more that gather rows
+constexpr int kGrTabWarps = 8;                   // warps that build the tile table
 constexpr int kGrGather = 128;
 constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
-constexpr int kGrSlab = 2 * 2 * 16 * 64 * 4;      // SwiGLU: two halves x (gate, up) x 16 columns x 64 rows, fp32
+constexpr int kGrSlab = 2 * 2 * 16 * 64 * 4;      // SwiGLU: two teams x (gate, up) x 16 columns x 64 rows, fp32
 constexpr int kFewRows = 64;
 
 // First row and number of rows of group e; offsets clamped to [0, P].
@@ -43,18 +44,21 @@ struct GroupedMmaParams {
   int m_tiles;                                   // tiles of 128 weight rows per group
 };
 
-template <int NMAX>
+// MB: 128-row blocks of weights per tile. Two share the tile's rows, which halves what has to be brought for them: with
+// one, 256-row tiles are bound by the copies (48 KB per 512 cycles of MMA), most of all where rows are gathered.
+template <int NMAX, int MB>
 struct GrGeom {
+  static constexpr int kA = MB * kGrABytes;
   static constexpr int kB = NMAX * 128;          // a stage of rows: NMAX rows x 64 K
-  static constexpr int kStage = kGrABytes + kB;
-  static constexpr int kStages = 192 * 1024 / kStage;      // 8 (64), 6 (128), 4 (256)
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = 192 * 1024 / kStage;      // 8 (64), 6 (128), 4 (256), 3 (256, two blocks)
   static constexpr int kBox = NMAX == 256 ? 128 : 64;      // rows of a TMA box of x
 };
 
 struct GrTab {
   int start[kGrMaxE + 1];                        // first tile of group e
   int off[kGrMaxE], cnt[kGrMaxE];
-  int wsum[kGrThreads / 32];
+  int wsum[kGrTabWarps];
   int pad;
 };
 static_assert(sizeof(GrTab) % 8 == 0, "the barriers behind it are 64-bit");
@@ -65,11 +69,13 @@ struct GrBars {
   int abort;
 };
 
-template <int NMAX>
+template <int NMAX, int MB>
 constexpr int gr_smem() {
-  return GrGeom<NMAX>::kStages * GrGeom<NMAX>::kStage + static_cast<int>(sizeof(GrTab) + sizeof(GrBars)) + kGrSlab + 1024;
+  return GrGeom<NMAX, MB>::kStages * GrGeom<NMAX, MB>::kStage + static_cast<int>(sizeof(GrTab) + sizeof(GrBars)) + kGrSlab + 1024;
 }
-static_assert(gr_smem<64>() <= 227 * 1024 && gr_smem<128>() <= 227 * 1024 && gr_smem<256>() <= 227 * 1024, "shared memory");
+static_assert(gr_smem<64, 1>() <= 227 * 1024 && gr_smem<128, 1>() <= 227 * 1024 && gr_smem<256, 1>() <= 227 * 1024 &&
+                  gr_smem<256, 2>() <= 227 * 1024,
+              "shared memory");
 
 struct GrTile {
   int e, m, row0, n;                             // group, weight tile, first row, rows (1..NMAX)
@@ -117,10 +123,11 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int it)
   for (int j = max(it - stages, 0); j < it; ++j) mbar_wait_bounded(&full[j % stages], (j / stages) & 1, 1000000);
 }
 
-// Warp 0: weights by TMA. Warp 1: MMA issue. Warp 2: rows by TMA, or warps 8-11 gather them. Warps 4-7: epilogue.
-template <int TYPE, int ACT, int NMAX, bool GATHER>
-__global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 1) grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
-  using G = GrGeom<NMAX>;
+// Warp 0: weights by TMA. Warp 1: MMA issue. Warp 2: rows by TMA, or the last four warps gather them. Warps 4-7 and 8-11:
+// epilogue, of 32 columns in turn or of a block each. One block has two sets of accumulators, two blocks have one.
+template <int TYPE, int ACT, int NMAX, bool GATHER, int MB>
+__global__ void __launch_bounds__(kGrThreads + (GATHER ? kGrGather : 0), 1) grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
+  using G = GrGeom<NMAX, MB>;
   const GroupedParams& p = mp.g;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bb.acc_full[a], 1);
-      mbar_init(&bb.acc_empty[a], 4);
+      mbar_init(&bb.acc_empty[a], 8);
     }
     mbar_init(&bb.done, 1);
     bb.abort = 0;
@@ -168,13 +175,13 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
     const int o = __shfl_up_sync(kAll, incl, d);
     if (lane >= d) incl += o;
   }
-  if (lane == 31 && warp < kGrThreads / 32) tt.wsum[warp] = incl;
+  if (lane == 31 && warp < kGrTabWarps) tt.wsum[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   int base = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kGrThreads / 32; ++w) {
+  for (int w = 0; w < kGrTabWarps; ++w) {
     if (w < warp) base += tt.wsum[w];
     total += tt.wsum[w];
   }
@@ -200,20 +207,23 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
             break;
           }
           uint8_t* st = sm + slot * G::kStage;
-          mbar_arrive_expect_tx(&bb.full[slot], kGrABytes);
-          if constexpr (ACT) {                   // 64 gate rows, then the 64 up rows of the same outputs
-            const int r = tl.e * p.N + tl.m * 64;
-            if (tl.once) {
-              tma_2d_hint(st, &mp.tm_w, s * 64, r, &bb.full[slot], pol);
-              tma_2d_hint(st + kGrABytes / 2, &mp.tm_w, s * 64, r + nout, &bb.full[slot], pol);
+          mbar_arrive_expect_tx(&bb.full[slot], G::kA);
+#pragma unroll
+          for (int b = 0; b < MB; ++b, st += kGrABytes) {
+            if constexpr (ACT) {                 // 64 gate rows, then the 64 up rows of the same outputs
+              const int r = tl.e * p.N + (tl.m * MB + b) * 64;
+              if (tl.once) {
+                tma_2d_hint(st, &mp.tm_w, s * 64, r, &bb.full[slot], pol);
+                tma_2d_hint(st + kGrABytes / 2, &mp.tm_w, s * 64, r + nout, &bb.full[slot], pol);
+              } else {
+                tma_2d(st, &mp.tm_w, s * 64, r, &bb.full[slot]);
+                tma_2d(st + kGrABytes / 2, &mp.tm_w, s * 64, r + nout, &bb.full[slot]);
+              }
+            } else if (tl.once) {
+              tma_2d_hint(st, &mp.tm_w, s * 64, tl.e * p.N + (tl.m * MB + b) * 128, &bb.full[slot], pol);
             } else {
-              tma_2d(st, &mp.tm_w, s * 64, r, &bb.full[slot]);
-              tma_2d(st + kGrABytes / 2, &mp.tm_w, s * 64, r + nout, &bb.full[slot]);
+              tma_2d(st, &mp.tm_w, s * 64, tl.e * p.N + (tl.m * MB + b) * 128, &bb.full[slot]);
             }
-          } else if (tl.once) {
-            tma_2d_hint(st, &mp.tm_w, s * 64, tl.e * p.N + tl.m * 128, &bb.full[slot], pol);
-          } else {
-            tma_2d(st, &mp.tm_w, s * 64, tl.e * p.N + tl.m * 128, &bb.full[slot]);
           }
         }
       }
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
             ok = false;
             break;
           }
-          uint8_t* st = sm + slot * G::kStage + kGrABytes;
+          uint8_t* st = sm + slot * G::kStage + G::kA;
           mbar_arrive_expect_tx(&bb.full[slot], boxes * G::kBox * 128);
           for (int b = 0; b < boxes; ++b)
             tma_2d(st + b * G::kBox * 128, &mp.tm_x, s * 64, tl.row0 + b * G::kBox, &bb.full[slot]);
@@ -244,7 +254,7 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
     // eight lanes per row of 128 bytes; a stage's barrier completes when every thread's copies have landed
     constexpr int kPass = NMAX / 16;
     const int tid = threadIdx.x - kGrThreads, c = tid & 7, r0 = tid >> 3;
-    const uint32_t dst0 = smem_u32(sm) + kGrABytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+    const uint32_t dst0 = smem_u32(sm) + G::kA + r0 * 128 + ((c ^ (r0 & 7)) << 4);
     int it = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -276,9 +286,9 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++ti) {
       const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
       const uint32_t idesc = idesc_m128((tl.n + 15) & ~15, TYPE == kTBf16);
-      const int as = ti & 1;
+      const int sets = MB == 1 ? 2 : 1, as = ti % sets;
       const uint32_t d = tmem + as * 256;
-      if (ti >= 2 && !pf_wait_all(&bb.acc_empty[as], ((ti >> 1) - 1) & 1, abort, &g_ops_error)) break;
+      if (ti >= sets && !pf_wait_all(&bb.acc_empty[as], (ti / sets - 1) & 1, abort, &g_ops_error)) break;
       tc_fence_after();
       for (int s = 0; s < steps; ++s, ++it) {
         const int slot = it % G::kStages;
@@ -288,41 +298,45 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
         }
         if constexpr (GATHER) fence_proxy_async_shared();     // the rows were written by ordinary (cp.async) copies
         tc_fence_after();
-        const uint32_t a0 = smem_u32(sm + slot * G::kStage), b0 = a0 + kGrABytes;
+        const uint32_t a0 = smem_u32(sm + slot * G::kStage), b0 = a0 + G::kA;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          tc_mma_ss_w(d, sdesc_sw128(a0 + ks * 32), sdesc_sw128(b0 + ks * 32), idesc, (s | ks) ? 1u : 0u);
+#pragma unroll
+          for (int b = 0; b < MB; ++b)
+            tc_mma_ss_w(d + b * 256, sdesc_sw128(a0 + b * kGrABytes + ks * 32), sdesc_sw128(b0 + ks * 32), idesc,
+                        (s | ks) ? 1u : 0u);
         tc_commit_w(&bb.empty[slot]);
       }
       if (ok) tc_commit_w(&bb.acc_full[as]);
     }
     tc_commit_w(&bb.done);
     pf_wait_all(&bb.done, 0, abort, &g_ops_error);
-  } else if (warp >= 4 && warp < 8) {
-    const int q = warp & 3;
+  } else if (warp >= 4 && warp < 12) {
+    const int q = warp & 3, team = (warp - 4) >> 2, blk = MB == 2 ? team : 0;
+    constexpr int kStep = MB == 2 ? 32 : 64;     // from 32 columns of a team to its next
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    int ti = 0, half = 0;
+    int ti = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       const GrTile tl = gr_tile<NMAX>(tt, p.E, t);
-      const int as = ti & 1;
-      const bool ok = pf_wait_all(&bb.acc_full[as], (ti >> 1) & 1, abort, &g_ops_error);
-      if (named_bar_or(1, 128, !ok)) break;      // the four warps give up together: they meet at barriers below
+      const int sets = MB == 1 ? 2 : 1, as = ti % sets;
+      const bool ok = pf_wait_all(&bb.acc_full[as], (ti / sets) & 1, abort, &g_ops_error);
+      if (named_bar_or(1 + team, 128, !ok)) break;           // a team gives up together: it meets at barriers below
       tc_fence_after();
-      const uint32_t d = lane_base + as * 256;
+      const uint32_t d = lane_base + (as + blk) * 256;
       if constexpr (ACT) {
         // warps 0, 1 hold the gate and 2, 3 the up values of the same 64 outputs: of 32 columns, each side hands 16
         // to the other through shared memory and finishes the other 16
-        const int r = 32 * (q & 1) + lane, n = tl.m * 64 + r, up = q >> 1;
-        for (int j0 = 0; j0 < tl.n; j0 += 32, half ^= 1) {
+        const int r = 32 * (q & 1) + lane, n = (tl.m * MB + blk) * 64 + r, up = q >> 1;
+        for (int j0 = MB == 2 ? 0 : 32 * team; j0 < tl.n; j0 += kStep) {
           uint32_t own[16], give[16];
           tc_ld16(d + j0 + 16 * up, own);
           tc_ld16(d + j0 + 16 * (up ^ 1), give);
           tc_wait_ld();
-          float* to = slab + ((half * 2 + up) * 16) * 64 + r;
-          const float* from = slab + ((half * 2 + (up ^ 1)) * 16) * 64 + r;
+          float* to = slab + ((team * 2 + up) * 16) * 64 + r;
+          const float* from = slab + ((team * 2 + (up ^ 1)) * 16) * 64 + r;
 #pragma unroll
           for (int c = 0; c < 16; ++c) to[c * 64] = __uint_as_float(give[c]);
-          named_bar_sync(1, 128);                // the next round writes the slab's other half
+          named_bar_sync(1 + team, 128);
           uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0 + 16 * up) * p.ldy + n;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -330,13 +344,14 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
             const float h = up ? silu_fast(o) * v : silu_fast(v) * o;
             if (j0 + 16 * up + c < tl.n && n < nout) yr[c * p.ldy] = from_f32<TYPE>(h);
           }
+          named_bar_sync(1 + team, 128);         // the slab is written again
         }
       } else {
-        for (int j0 = 0; j0 < tl.n; j0 += 16) {
+        for (int j0 = MB == 2 ? 0 : 32 * team; j0 < tl.n; j0 += (j0 & 16) ? kStep - 16 : 16) {
           uint32_t v[16];
           tc_ld16(d + j0, v);
           tc_wait_ld();
-          const int n = tl.m * 128 + 32 * q + lane;
+          const int n = (tl.m * MB + blk) * 128 + 32 * q + lane;
           uint16_t* yr = p.y + static_cast<long long>(tl.row0 + j0) * p.ldy + n;
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -355,22 +370,23 @@ __global__ void __launch_bounds__(GATHER ? kGrThreads + kGrGather : kGrThreads, 
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int TYPE, int ACT, int NMAX, bool GATHER>
+template <int TYPE, int ACT, int NMAX, bool GATHER, int MB = 1>
 cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s) {
   GroupedMmaParams mp;
   mp.g = p;
   const int nout = ACT ? p.N / 2 : p.N;
-  mp.m_tiles = ACT ? (nout + 63) / 64 : (nout + 127) / 128;
+  mp.m_tiles = (nout + (ACT ? 64 : 128) * MB - 1) / ((ACT ? 64 : 128) * MB);
   if (!encode_16bit(&mp.tm_w, p.w, TYPE == kTBf16, static_cast<uint64_t>(p.E) * p.N, p.K, p.K, ACT ? 64 : 128) ||
-      (!GATHER && !encode_16bit(&mp.tm_x, p.x, TYPE == kTBf16, p.x_rows, p.K, p.ldx, GrGeom<NMAX>::kBox)))
+      (!GATHER && !encode_16bit(&mp.tm_x, p.x, TYPE == kTBf16, p.x_rows, p.K, p.ldx, GrGeom<NMAX, MB>::kBox)))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem_once<grouped_mma_kernel<TYPE, ACT, NMAX, GATHER>>(dev, gr_smem<NMAX>());
+  cudaError_t e = allow_smem_once<grouped_mma_kernel<TYPE, ACT, NMAX, GATHER, MB>>(dev, gr_smem<NMAX, MB>());
   if (e != cudaSuccess) return e;
   // tiles that the rows can make at most
   const long long chunks = p.P / NMAX + (p.E < p.P ? p.E : p.P);
   const long long most = chunks * mp.m_tiles;
-  grouped_mma_kernel<TYPE, ACT, NMAX, GATHER><<<most < sms ? static_cast<int>(most) : sms,
-                                                GATHER ? kGrThreads + kGrGather : kGrThreads, gr_smem<NMAX>(), s>>>(mp);
+  grouped_mma_kernel<TYPE, ACT, NMAX, GATHER, MB><<<most < sms ? static_cast<int>(most) : sms,
+                                                    kGrThreads + (GATHER ? kGrGather : 0),
+                                                    gr_smem<NMAX, MB>(), s>>>(mp);
   return cudaGetLastError();
 }
 
@@ -630,6 +646,12 @@ cudaError_t launch_type(const GroupedParams& p, cudaStream_t s) {
   const bool ga = p.row_of != nullptr;
   if (mean <= 64) return ga ? launch_mma<TYPE, ACT, 64, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 64, false>(p, dev, sms, s);
   if (mean <= 128) return ga ? launch_mma<TYPE, ACT, 128, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 128, false>(p, dev, sms, s);
+  // Two blocks where rows are gathered and the tiles then still fill the SMs: 16384 tokens over 256 experts, gate|up,
+  // 642 -> 463 us, 4096^3 173 -> 120 us. Rows by TMA gain less (110 -> 104 us) or lose to the accumulators' single set
+  // (SwiGLU, 8 experts: 177 -> 197 us).
+  const int nout = ACT ? p.N / 2 : p.N;
+  const long long chunks = p.P / 256 > p.E ? p.P / 256 : p.E, wide = (nout + (ACT ? 127 : 255)) / (ACT ? 128 : 256);
+  if (ga && wide * chunks * 2 >= 3 * sms) return launch_mma<TYPE, ACT, 256, true, 2>(p, dev, sms, s);
   return ga ? launch_mma<TYPE, ACT, 256, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 256, false>(p, dev, sms, s);
 }
 

@@ -221,6 +221,14 @@ def test_grouped_many_rows(i, act, dtype):
     grouped_check(MANY[i], N, K, dtype, act, 50 + i, gather=i % 2 == 0, pad=8 * (i % 3), tail=3 * (i % 2), row_div=1 + i % 4)
 
 
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("gather", [True, False])
+def test_grouped_large_groups(act, gather):
+    # several hundred rows per group and enough weight tiles that two blocks of them share the rows
+    grouped_check([700, 0, 300, 513, 40], 5000 if act else 4900, 136, torch.bfloat16, act, 11, gather=gather, tail=5, row_div=2)
+    grouped_check([1030], 6000, 72, torch.float16, act, 12, gather=gather)
+
+
 def test_grouped_many_experts_and_odd_widths():
     rng = np.random.default_rng(0)
     counts = rng.integers(0, 4, 1024)
