@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const i
 
   for (int i = threadIdx.x; i < nw * E; i += blockDim.x) cnt[i] = 0;
   __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   const long long lo_ll = static_cast<long long>(rank * nw + warp) * wlen;
   const int lo = static_cast<int>(min(lo_ll, static_cast<long long>(P)));
   const int hi = static_cast<int>(min(lo_ll + wlen, static_cast<long long>(P)));
@@ -129,6 +131,8 @@ __global__ void __launch_bounds__(kPermMaxThreads) expert_permute_kernel(const i
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256, 4) expert_combine_kernel(const __grid_constant__ CombineParams p) {
   constexpr int kCols = VEC ? 8 : 1;
+  pdl_wait();
+  pdl_trigger();
   const long long t = blockIdx.x;
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kCols;
   if (c >= p.H) return;
@@ -232,9 +236,8 @@ cudaError_t launch_combine_type(const CombineParams& p, cudaStream_t s) {
   const int threads = units >= 256 ? 256 : (units + 31) / 32 * 32;
   const dim3 grid(p.T, (units + threads - 1) / threads);
   if (grid.y > 65535) return cudaErrorInvalidConfiguration;
-  if (vec) expert_combine_kernel<TYPE, true><<<grid, threads, 0, s>>>(p);
-  else expert_combine_kernel<TYPE, false><<<grid, threads, 0, s>>>(p);
-  return cudaGetLastError();
+  return vec ? launch_op(expert_combine_kernel<TYPE, true>, grid, threads, 0, s, p)
+             : launch_op(expert_combine_kernel<TYPE, false>, grid, threads, 0, s, p);
 }
 
 }  // namespace
@@ -255,13 +258,15 @@ cudaError_t launch_expert_permute(const int* ids, int P, int E, int* offsets, in
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = 4 * (2 * E + 1 + threads / 32 * E);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ncta;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, expert_permute_kernel, ids, P, E, wlen, offsets, perm, inv);
 }
 

@@ -156,6 +156,8 @@ __global__ void __launch_bounds__(kGrThreads + (GATHER ? kGrGather : 0), 1) grou
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bb.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  pdl_wait();
+  pdl_trigger();
   // tile table: thread i owns the groups 4i..4i+3
   int tiles4 = 0, first4[4];
 #pragma unroll
@@ -384,10 +386,8 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
   // tiles that the rows can make at most
   const long long chunks = p.P / NMAX + (p.E < p.P ? p.E : p.P);
   const long long most = chunks * mp.m_tiles;
-  grouped_mma_kernel<TYPE, ACT, NMAX, GATHER, MB><<<most < sms ? static_cast<int>(most) : sms,
-                                                    kGrThreads + (GATHER ? kGrGather : 0),
-                                                    gr_smem<NMAX, MB>(), s>>>(mp);
-  return cudaGetLastError();
+  return launch_op(grouped_mma_kernel<TYPE, ACT, NMAX, GATHER, MB>, dim3(most < sms ? static_cast<int>(most) : sms),
+                   kGrThreads + (GATHER ? kGrGather : 0), gr_smem<NMAX, MB>(), s, mp);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -446,6 +446,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   uint8_t* ring = align1024(smem_raw);
   float4* red = reinterpret_cast<float4*>(ring + ge.stages * kFewStage);       // [warps][NT][32]
 
+  pdl_wait();
+  pdl_trigger();
   // active groups in ascending order: thread i looks at the groups 2i, 2i + 1
   int2 span[2];
   int n = 0;
@@ -628,8 +630,7 @@ cudaError_t launch_few(const GroupedParams& p, int dev, int sms, cudaStream_t s)
   if (!(fp.blocks ? encode_16bit_blocks(&fp.tm, p.w, TYPE == kTBf16, rows, p.K, p.K, box, 2 * fp.kw)
                   : encode_16bit(&fp.tm, p.w, TYPE == kTBf16, rows, p.K, p.K, box)))
     return cudaErrorInvalidValue;
-  grouped_few_kernel<TYPE, ACT, NT><<<sms, kFewThreads, kSmem, s>>>(fp);
-  return cudaGetLastError();
+  return launch_op(grouped_few_kernel<TYPE, ACT, NT>, dim3(sms), kFewThreads, kSmem, s, fp);
 }
 
 template <int TYPE, int ACT>

@@ -110,6 +110,8 @@ constexpr int kMaxThreads = VPT == 1 ? 1024 : VPT == 8 ? 512 : 256;
 template <int TYPE, bool RES_F32, bool VEC, int VPT>
 __global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float sum_post[kNormWarps], sum_pre[kNormWarps];
+  pdl_wait();
+  pdl_trigger();
   const long long t = blockIdx.x;
   const int H = p.H;
   float x[VPT][8];
@@ -211,12 +213,11 @@ cudaError_t launch_vpt(const NormParams& p, cudaStream_t s) {
   const int vpt = n8 > 1024 ? 8 : p.T >= 1024 && n8 > 512 ? 4 : p.T >= 1024 && n8 > 256 ? 2 : 1;
   const int threads = ((n8 + vpt - 1) / vpt + 31) / 32 * 32;
   switch (vpt) {
-    case 1: block_norm_kernel<TYPE, RES_F32, VEC, 1><<<p.T, threads, 0, s>>>(p); break;
-    case 2: block_norm_kernel<TYPE, RES_F32, VEC, 2><<<p.T, threads, 0, s>>>(p); break;
-    case 4: block_norm_kernel<TYPE, RES_F32, VEC, 4><<<p.T, threads, 0, s>>>(p); break;
-    default: block_norm_kernel<TYPE, RES_F32, VEC, 8><<<p.T, threads, 0, s>>>(p); break;
+    case 1: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 1>, dim3(p.T), threads, 0, s, p);
+    case 2: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 2>, dim3(p.T), threads, 0, s, p);
+    case 4: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 4>, dim3(p.T), threads, 0, s, p);
+    default: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 8>, dim3(p.T), threads, 0, s, p);
   }
-  return cudaGetLastError();
 }
 
 template <int TYPE>

@@ -103,6 +103,23 @@ __device__ __forceinline__ void st_cluster_f32(float* p, int rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
+// Launches an operator's kernel as a programmatic dependent of what runs before it in the stream: its launch overlaps
+// that kernel's end, and it calls pdl_wait before it touches memory (then pdl_trigger, for the next one).
+template <typename Kern, typename... Args>
+cudaError_t launch_op(Kern kernel, dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // 16-bit element of an activation tensor as fp32, and back (one rounding, to nearest even)
 template <int TYPE>
 __device__ __forceinline__ float to_f32(uint16_t b) {

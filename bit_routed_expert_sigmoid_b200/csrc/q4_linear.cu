@@ -161,6 +161,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
     }
     __syncthreads();
   }
+  // Behind the operand kernel the weights may be read at once: it has waited for all that ran before it.
+  if constexpr (INLINE) pdl_wait();
+  pdl_trigger();
   if (warp == kQ4Warps) {
     if (TMA && lane == 0) {
       // weights are no predecessor's output: copied before griddepcontrol.wait; x is the operand kernel's
@@ -428,7 +431,7 @@ cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = INLINE ? 0 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, q4_ring_kernel<AR, TYPE, NT, RB, TMA, INLINE>, rp);
 }
 

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bb.tmem, tmem_a = tmem + kMmD * 64;
+  pdl_trigger();
   const int half = (warp - kMmSums) >> 2;             // sums: which 16 of every 32 tokens
   float acc[kMmTokens / 2];                      // sums: tokens 16 (2 b + half) + j at 16 b + j
 #pragma unroll
