@@ -20,7 +20,8 @@ namespace {
 enum Arith : int { kF16Int4, kF16Nvfp4, kLimbs };
 
 // A (token, segment) is four chunks of 16 bytes for each of the four lanes q that read it, K = 32 q .. 32 q + 31. fp16:
-// chunk i holds K = 32 q + 8 i .. + 7 (int4: in the order of the decoded pairs, 0,4,1,5,2,6,3,7); limbs: chunk 2 limb +
+// chunk i holds K = 32 q + 8 i .. + 7 in the order of the decoded pairs (int4 0,4,1,5,2,6,3,7; NVFP4 0,1,2,6,4,5,3,7);
+// limbs: chunk 2 limb +
 // (i >> 1) holds at 8 (i & 1) the bytes of K = 32 q + 8 i + 0, 2, 4, 6 and of + 1, 3, 5, 7.
 //   kTokens  [segment][token][chunk][q], then the inverse factor, kTokenBytes each
 //   kTiles   [segment][tile of 8 tokens][chunk][token][q], kTileBytes each; then the factors [segment][tile][8]
@@ -140,8 +141,11 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
         const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j][1] : v[j][3], 1);
         u = odd ? make_uint2(pack_half2(r0, v[j][2]), pack_half2(r1, v[j][3]))
                 : make_uint2(pack_half2(v[j][0], r0), pack_half2(v[j][1], r1));
-      } else {
-        u = make_uint2(pack_half2(v[j][0], v[j][1]), pack_half2(v[j][2], v[j][3]));
+      } else {                                   // 0,1,2,6 by the even lane of a pair, 4,5,3,7 by the odd one
+        const float r = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j][2] : v[j][3], 1);
+        u = odd ? make_uint2(pack_half2(v[j][0], v[j][1]), pack_half2(r, v[j][3]))
+                : make_uint2(pack_half2(v[j][0], v[j][1]), pack_half2(v[j][2], r));
+        inv *= 128.f;                            // see decode_f16
       }
       off = c * o[j].chunk + 8 * odd;
     }
@@ -190,10 +194,16 @@ __device__ __forceinline__ void decode_f16(const uint4& c, uint32_t s2, uint32_t
 #pragma unroll
       for (int j = 0; j < 4; ++j) d[4 * i + j] = pr[j];
     } else {
-      const uint32_t h = e4m3_to_half_bits((s2 >> (8 * (i >> 1))) & 0xFFu);
-      const uint32_t hh = h | (h << 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[4 * i + j] = hmul2_u32(e2m1x2_to_half2(w[i] >> (8 * j)), hh);
+      // Codes 0, 1 and 4, 5 by the hardware conversion, the pairs 2, 6 and 3, 7 by moving their bits: sign to bit 15,
+      // exponent and fraction to bits 11-9, which is the value times 2^-14 (subnormals included). Both kinds of work
+      // then run side by side. The products with the scale times 2^-7 and 2^7 are exact and share a factor of 2^-7.
+      const uint32_t h = e4m3_to_half_bits((s2 >> (8 * (i >> 1))) & 0xFFu), hh = h | (h << 16);
+      const uint32_t up = hmul2_u32(hh, 0x58005800u), down = hmul2_u32(hh, 0x20002000u);       // 2^7, 2^-7
+      const uint32_t u = w[i] << 4;
+      d[4 * i] = hmul2_u32(e2m1x2_to_half2(w[i]), down);
+      d[4 * i + 1] = hmul2_u32((u & 0x80008000u) | ((u >> 3) & 0x0E000E00u), up);
+      d[4 * i + 2] = hmul2_u32(e2m1x2_to_half2(w[i] >> 16), down);
+      d[4 * i + 3] = hmul2_u32((w[i] & 0x80008000u) | ((w[i] >> 3) & 0x0E000E00u), up);
     }
   }
 }
