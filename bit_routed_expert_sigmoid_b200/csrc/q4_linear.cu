@@ -129,14 +129,14 @@ struct RingBars {
 // Bytes of a block's rows in a stage: whole swizzle atoms, so that a lane's place in them is the same in every block.
 __host__ __device__ inline int ring_region(int kw, int R) { return ((kw + 1) / 2 * R * 128 + 1023) & ~1023; }
 
-template <int AR, int TYPE, int NT, int RB, bool TMA, bool INLINE>
+template <int AR, int TYPE, int RB, bool TMA, bool INLINE>
 __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_constant__ RingParams rp) {
   const Q4Params& p = rp.q;
   extern __shared__ uint8_t smem_raw[];
   __shared__ RingBars bb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int segs = (p.K + 127) / 128, teams = kQ4Warps / rp.kw, chunks = (segs + rp.kw - 1) / rp.kw;
-  constexpr bool kXRing = TMA && NT == 1 && !INLINE;             // x through the ring
+  constexpr bool kXRing = TMA && !INLINE;                        // x through the ring
   const int R = rp.R, kbs = (rp.kw + 1) / 2, region = ring_region(rp.kw, R);
   const int xstage = kXRing ? rp.kw * p.T * kTokenBytes : 0;
   const int stage = (teams * RB * region + xstage + 1023) & ~1023;
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
   constexpr bool kI4 = AR != kF16Nvfp4;
   const size_t scale_row = kI4 ? p.K >> 6 : p.K >> 4;            // bytes
   uint8_t* ring = align1024(smem_raw);
-  float4* red = reinterpret_cast<float4*>(ring + rp.stages * stage);           // [warps][RB][NT][32]
-  uint8_t* sm_scales = reinterpret_cast<uint8_t*>(red + kQ4Warps * RB * NT * 32);
+  float4* red = reinterpret_cast<float4*>(ring + rp.stages * stage);           // [warps][RB][32]
+  uint8_t* sm_scales = reinterpret_cast<uint8_t*>(red + kQ4Warps * RB * 32);
   uint8_t* sm_x = sm_scales + rp.scale_bytes;                    // INLINE: the operand
   volatile int* abort = &bb.abort;
 
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
     }
     __syncthreads();
   }
-  // Behind the operand kernel the weights may be read at once: it has waited for all that ran before it.
+  // Behind the operand kernel the weights may be read at once: all that ran before that one is complete.
   if constexpr (INLINE) pdl_wait();
   pdl_trigger();
   if (warp == kQ4Warps) {
@@ -216,10 +216,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
   }
 
   const int kw = warp % rp.kw, team = warp / rp.kw, tid = kw * 32 + lane;
-  const int t0 = blockIdx.y * 8 * NT, tiles = (p.T + 7) / 8;
-  const int ntile = min(NT, (p.T - t0 + 7) / 8);
   const uint8_t* img = static_cast<const uint8_t*>(p.workspace);
-  const float* fac = reinterpret_cast<const float*>(img + static_cast<size_t>(tiles) * segs * kTileBytes);
 
   // the lane's place in a block: row g + 8 h (the last one repeated behind the block's end), its 16 bytes
   uint32_t place[2];
@@ -283,38 +280,25 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
 
   int it = 0;
   for (int rd = 0; rd < rounds; ++rd) {
-    float acc[RB][NT][4];
+    float acc[RB][4];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.f;
+      for (int j = 0; j < 4; ++j) acc[r][j] = 0.f;
     for (int c = 0; c < chunks; ++c, ++it) {
       const int slot = it % rp.stages, seg = c * rp.kw + kw;
-      uint4 x[4];
-      float2 fx;
-      auto load_x = [&](int t) {
-        if constexpr (NT == 1) {                 // lanes behind the last token repeat it: their columns are not used
-          const uint8_t* xs = INLINE ? sm_x + seg * p.T * kTokenBytes
-                              : TMA  ? ring + slot * stage + teams * RB * region + kw * p.T * kTokenBytes
-                                     : img + static_cast<size_t>(seg) * p.T * kTokenBytes;
-          const uint8_t* xb = xs + min(g, p.T - 1) * kTokenBytes + 16 * q;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(xb + 64 * i);
-          fx.x = *reinterpret_cast<const float*>(xs + min(2 * q, p.T - 1) * kTokenBytes + 256);
-          fx.y = *reinterpret_cast<const float*>(xs + min(2 * q + 1, p.T - 1) * kTokenBytes + 256);
-        } else {
-          const size_t tile = static_cast<size_t>(seg) * tiles + (t0 >> 3) + t;
-          const uint4* xb = reinterpret_cast<const uint4*>(img + tile * kTileBytes) + lane;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = xb[32 * i];
-          fx = *reinterpret_cast<const float2*>(fac + tile * 8 + 2 * q);
-        }
-      };
       if constexpr (TMA) ok = ok && pf_wait_all(&bb.full[slot], (it / rp.stages) & 1, abort, &g_ops_error_q4);
       if (seg < segs && ok) {
-        if constexpr (NT == 1) load_x(0);
+        // lanes behind the last token repeat it: their columns are not used
+        const uint8_t* xs = INLINE ? sm_x + seg * p.T * kTokenBytes
+                            : TMA  ? ring + slot * stage + teams * RB * region + kw * p.T * kTokenBytes
+                                   : img + static_cast<size_t>(seg) * p.T * kTokenBytes;
+        const uint8_t* xb = xs + min(g, p.T - 1) * kTokenBytes + 16 * q;
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(xb + 64 * i);
+        const float fx = *reinterpret_cast<const float*>(xs + min(2 * q, p.T - 1) * kTokenBytes + 256);
+        const float fy = *reinterpret_cast<const float*>(xs + min(2 * q + 1, p.T - 1) * kTokenBytes + 256);
         if (resident) {
 #pragma unroll
           for (int r = 0; r < RB; ++r)
@@ -342,18 +326,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
           a.decode(code, sc[r]);
           const float s0 = kI4 ? bf16_bits_to_f32(static_cast<uint16_t>(sc[r][0])) : 1.f;
           const float s1 = kI4 ? bf16_bits_to_f32(static_cast<uint16_t>(sc[r][1])) : 1.f;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (NT == 1 || t < ntile) {
-              if constexpr (NT > 1) load_x(t);
-              float d[4];
-              a.times(x, d);
-              acc[r][t][0] = fmaf(d[0], s0 * fx.x, acc[r][t][0]);
-              acc[r][t][1] = fmaf(d[1], s0 * fx.y, acc[r][t][1]);
-              acc[r][t][2] = fmaf(d[2], s1 * fx.x, acc[r][t][2]);
-              acc[r][t][3] = fmaf(d[3], s1 * fx.y, acc[r][t][3]);
-            }
-          }
+          float d[4];
+          a.times(x, d);
+          acc[r][0] = fmaf(d[0], s0 * fx, acc[r][0]);
+          acc[r][1] = fmaf(d[1], s0 * fy, acc[r][1]);
+          acc[r][2] = fmaf(d[2], s1 * fx, acc[r][2]);
+          acc[r][3] = fmaf(d[3], s1 * fy, acc[r][3]);
         }
         if (seg + rp.kw < segs) {
           if (!resident) load_scales(seg + rp.kw);
@@ -369,32 +347,29 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
     }
     if (kw < segs) {
 #pragma unroll
-      for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          red[((warp * RB + r) * NT + t) * 32 + lane] = make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
+      for (int r = 0; r < RB; ++r) red[(warp * RB + r) * 32 + lane] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
     }
     if (named_bar_or(team, 32 * rp.kw, !ok)) break;              // a team gives up together
     // add the team's partial sums in warp order
-    const float* rf = reinterpret_cast<const float*>(red) + team * rp.kw * RB * NT * 128;
+    const float* rf = reinterpret_cast<const float*>(red) + team * rp.kw * RB * 128;
     const int parts = min(rp.kw, segs);
-    for (int o = tid; o < RB * NT * 128; o += 32 * rp.kw) {
-      const int row = o & 15, tok = (o >> 4) % (8 * NT), r = o / (128 * NT);
+    for (int o = tid; o < RB * 128; o += 32 * rp.kw) {
+      const int row = o & 15, t = (o >> 4) & 7, r = o >> 7;
       const int n = (first + (rd * teams + team) * RB + r) * R + row;
-      if (t0 + tok >= p.T || row >= R || n >= p.N) continue;
-      const int at = ((r * NT + (tok >> 3)) * 32 + (row & 7) * 4 + ((tok & 7) >> 1)) * 4 + (row >> 3) * 2 + (tok & 1);
+      if (t >= p.T || row >= R || n >= p.N) continue;
+      const int at = (r * 32 + (row & 7) * 4 + (t >> 1)) * 4 + (row >> 3) * 2 + (t & 1);
       float v = 0.f;
 #pragma unroll 4
-      for (int w = 0; w < parts; ++w) v += rf[at + w * RB * NT * 128];
-      p.y[static_cast<long long>(t0 + tok) * p.ldy + n] = from_f32<TYPE>(v * ts);
+      for (int w = 0; w < parts; ++w) v += rf[at + w * RB * 128];
+      p.y[t * p.ldy + n] = from_f32<TYPE>(v * ts);
     }
     named_bar_sync(team, 32 * rp.kw);
   }
 }
 
-template <int AR, int TYPE, int NT, int RB, bool TMA, bool INLINE>
+template <int AR, int TYPE, int RB, bool TMA, bool INLINE>
 cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_t s) {
-  constexpr int kRed = kQ4Warps * RB * NT * 512, kMost = 226 * 1024 - static_cast<int>(sizeof(RingBars));
+  constexpr int kRed = kQ4Warps * RB * 512, kMost = 226 * 1024 - static_cast<int>(sizeof(RingBars));
   const int segs = (p.K + 127) / 128, teams = kQ4Warps / kw;
   RingParams rp;
   rp.q = p;
@@ -406,7 +381,7 @@ cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_
   const long long scale_row = kI4 ? p.K >> 6 : p.K >> 4, scale_all = (rp.blocks * rp.R * scale_row + 127) & ~127ll;
   const bool sc16 = scale_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0;
   rp.scale_bytes = TMA && sc16 && scale_all <= kQ4ScaleBytes ? static_cast<int>(scale_all) : 0;
-  const int xstage = TMA && NT == 1 && !INLINE ? kw * p.T * kTokenBytes : 0;
+  const int xstage = TMA && !INLINE ? kw * p.T * kTokenBytes : 0;
   const int stage = (teams * RB * ring_region(kw, rp.R) + xstage + 1023) & ~1023;
   const int rest = kRed + 1024 + rp.scale_bytes + (INLINE ? static_cast<int>(q4_operand_bytes(p.T, segs)) : 0);
   rp.stages = 0;
@@ -419,11 +394,11 @@ cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_
                    : encode_words(&rp.tm, p.codes, p.N, p.K / 2, rp.R)))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = allow_smem_once<q4_ring_kernel<AR, TYPE, NT, RB, TMA, INLINE>>(dev, kMost);
+  cudaError_t e = allow_smem_once<q4_ring_kernel<AR, TYPE, RB, TMA, INLINE>>(dev, kMost);
   if (e != cudaSuccess) return e;
   const int total = (p.N + rp.R - 1) / rp.R;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((total + rp.blocks - 1) / rp.blocks, (p.T + 8 * NT - 1) / (8 * NT));
+  cfg.gridDim = dim3((total + rp.blocks - 1) / rp.blocks);
   cfg.blockDim = dim3(kRingThreads);
   cfg.dynamicSmemBytes = rp.stages * stage + rest;
   cfg.stream = s;
@@ -432,18 +407,18 @@ cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q4_ring_kernel<AR, TYPE, NT, RB, TMA, INLINE>, rp);
+  return cudaLaunchKernelEx(&cfg, q4_ring_kernel<AR, TYPE, RB, TMA, INLINE>, rp);
 }
 
 // Blocks of rows that a team works on at a time: two, sharing a segment's x, where there are as many.
-template <int AR, int TYPE, int NT, bool TMA, bool INLINE>
+template <int AR, int TYPE, bool TMA, bool INLINE>
 cudaError_t launch_ring(const Q4Params& p, int dev, int sms, cudaStream_t s) {
   const int segs = (p.K + 127) / 128;
   int kw = 1;
   while (kw < segs && kw < kQ4Split) kw *= 2;
   const int blocks = ((p.N + sms - 1) / sms + 15) / 16, teams = kQ4Warps / kw;
-  if (blocks <= teams) return launch_rows<AR, TYPE, NT, 1, TMA, INLINE>(p, dev, sms, kw, s);
-  return launch_rows<AR, TYPE, NT, 2, TMA, INLINE>(p, dev, sms, kw, s);
+  if (blocks <= teams) return launch_rows<AR, TYPE, 1, TMA, INLINE>(p, dev, sms, kw, s);
+  return launch_rows<AR, TYPE, 2, TMA, INLINE>(p, dev, sms, kw, s);
 }
 
 template <int AR, int TYPE, bool TMA>
@@ -451,12 +426,9 @@ cudaError_t launch_tokens(const Q4Params& p, cudaStream_t s) {
   int dev, sms;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  if (q4_workspace_bytes(p.K, p.T) == 0) return launch_ring<AR, TYPE, 1, TMA, true>(p, dev, sms, s);
-  if (p.T <= 8) {
-    if ((e = launch_q4_operand<AR, TYPE, kTokens>(p, sms, s)) != cudaSuccess) return e;
-    return launch_ring<AR, TYPE, 1, TMA, false>(p, dev, sms, s);
-  }
-  return launch_q4_mma(p, s);
+  if (q4_workspace_bytes(p.K, p.T) == 0) return launch_ring<AR, TYPE, TMA, true>(p, dev, sms, s);
+  if ((e = launch_q4_operand<AR, TYPE, kTokens>(p, sms, s)) != cudaSuccess) return e;
+  return launch_ring<AR, TYPE, TMA, false>(p, dev, sms, s);
 }
 
 template <int AR, bool TMA>
@@ -483,6 +455,7 @@ size_t q4_workspace_bytes(int K, int T) {
 }
 
 cudaError_t launch_q4_linear(const Q4Params& p, cudaStream_t s) {
+  if (p.T > 8) return launch_q4_mma(p, s);
   if (p.fmt == kInt4) return p.rotated ? launch_type<kLimbs, true>(p, s) : launch_type<kF16Int4, true>(p, s);
   // 16-byte rows of codes and 2-byte aligned pairs of scales where the width and the pointer allow
   const bool tma = p.K % 32 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 1u) == 0;
