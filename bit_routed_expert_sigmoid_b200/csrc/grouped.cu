@@ -25,7 +25,7 @@ constexpr int kGrTabWarps = 8;                   // warps that build the tile ta
 constexpr int kGrGather = 128;
 constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
 constexpr int kGrSlab = 2 * 2 * 16 * 64 * 4;      // SwiGLU: two teams x (gate, up) x 16 columns x 64 rows, fp32
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 
 // First row and number of rows of group e; offsets clamped to [0, P].
 __device__ __forceinline__ int2 group_span(const int* offsets, int e, int P) {
@@ -410,7 +410,7 @@ constexpr int kFewMaxStages = 8;
 
 struct FewTab {
   uint64_t full[kFewMaxStages], empty[kFewMaxStages];
-  int n_active, abort;
+  int pad, abort;
   int wsum[kFewWarps + 1];
   int e[kFewRows], off[kFewRows], cnt[kFewRows];
   int src[kFewRows];                             // row of x of each row of y
@@ -433,7 +433,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
   else mma_f16_16816(d, a, b0, b1);
 }
 
-template <int TYPE, int ACT, int NT>
+template <int TYPE, int ACT>
 __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __grid_constant__ FewParams ge) {
   const GroupedParams& p = ge.g;
   constexpr int kUnit = ACT ? 8 : 16;            // outputs per unit
@@ -444,18 +444,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   const int units_per = (nout + kUnit - 1) / kUnit;
   const int teams = kFewWarps / ge.kw;
   uint8_t* ring = align1024(smem_raw);
-  float4* red = reinterpret_cast<float4*>(ring + ge.stages * kFewStage);       // [warps][NT][32]
+  float4* red = reinterpret_cast<float4*>(ring + ge.stages * kFewStage);       // [warps][32]
 
   pdl_wait();
   pdl_trigger();
-  // active groups in ascending order: thread i looks at the groups 2i, 2i + 1
+  // entries of up to eight rows of a group, in ascending order: thread i looks at the groups 2i, 2i + 1
   int2 span[2];
   int n = 0;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * threadIdx.x + j;
     span[j] = e < p.E ? group_span(p.offsets, e, p.P) : make_int2(0, 0);
-    n += span[j].y > 0;
+    n += (span[j].y + 7) / 8;
   }
   int incl = n;
 #pragma unroll
@@ -482,17 +482,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    if (span[j].y > 0) {
+    for (int i = 0; i < span[j].y; i += 8, ++at)
       if (at < kFewRows) {                       // groups that overlap (bad offsets) may be more: left out
         tab.e[at] = 2 * threadIdx.x + j;
-        tab.off[at] = span[j].x;
-        tab.cnt[at] = span[j].y;
+        tab.off[at] = span[j].x + i;
+        tab.cnt[at] = min(span[j].y - i, 8);
       }
-      ++at;
-    }
   __syncthreads();
-  const int n_active = min(total, kFewRows);
-  const long long units = static_cast<long long>(n_active) * units_per;
+  const long long units = static_cast<long long>(min(total, kFewRows)) * units_per;
   const int u_lo = static_cast<int>(units * blockIdx.x / gridDim.x);
   const int u_hi = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
   const int chunk = 128 * ge.kw, chunks = (p.K + chunk - 1) / chunk;
@@ -537,18 +534,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   }
 
   const int kw = warp % ge.kw, team = warp / ge.kw, tid = kw * 32 + lane;
-  const float* rf = reinterpret_cast<const float*>(red) + team * ge.kw * NT * 128;
+  const float* rf = reinterpret_cast<const float*>(red) + team * ge.kw * 128;
   int it = 0;
-  int ai = (u_lo + team) / units_per, un = u_lo + team - ai * units_per;       // unit `un` of active group ai
+  int ai = (u_lo + team) / units_per, un = u_lo + team - ai * units_per;       // unit `un` of entry ai
   bool ok = true;
   for (int u0 = u_lo; u0 < u_hi; u0 += teams) {
     const bool mine = u0 + team < u_hi;
-    const int cnt = mine ? min(tab.cnt[ai], 8 * NT) : 0, off = mine ? tab.off[ai] : 0;
-    float acc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+    const int cnt = mine ? tab.cnt[ai] : 0, off = mine ? tab.off[ai] : 0;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c = 0; c < chunks; ++c, ++it) {
       const int slot = it % ge.stages, k0 = c * chunk + kw * 128 + 8 * q;
       ok = ok && pf_wait_all(&tab.full[slot], (it / ge.stages) & 1, abort, &g_ops_error);
@@ -564,39 +557,32 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
           a[i] = *reinterpret_cast<const uint4*>(lo + at);
           a[4 + i] = *reinterpret_cast<const uint4*>(hi + at);
         }
+        const bool tok = g < cnt;
+        const uint16_t* x = p.x + (tok ? tab.src[off + g] * p.ldx : 0) + k0;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};       // two chains
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (8 * t < cnt) {
-            const bool tok = 8 * t + g < cnt;
-            const uint16_t* x = p.x + (tok ? tab.src[off + 8 * t + g] * p.ldx : 0) + k0;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};   // two chains
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (tok && k0 + 32 * i < p.K) v = ld_nc_v4(x + 32 * i);
-              mma_16816<TYPE>(acc[t], a[i].x, a[4 + i].x, a[i].y, a[4 + i].y, v.x, v.y);
-              mma_16816<TYPE>(d, a[i].z, a[4 + i].z, a[i].w, a[4 + i].w, v.z, v.w);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[t][j] += d[j];
-          }
+        for (int i = 0; i < 4; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (tok && k0 + 32 * i < p.K) v = ld_nc_v4(x + 32 * i);
+          mma_16816<TYPE>(acc, a[i].x, a[4 + i].x, a[i].y, a[4 + i].y, v.x, v.y);
+          mma_16816<TYPE>(d, a[i].z, a[4 + i].z, a[i].w, a[4 + i].w, v.z, v.w);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += d[j];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&tab.empty[slot]);
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if (8 * t < cnt) red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    if (cnt) red[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     if (named_bar_or(team, 32 * ge.kw, !ok)) break;            // a team gives up together
     const int j = tid % kUnit, nn = un * kUnit + j;
     if (nn < nout)
       for (int tok = tid / kUnit; tok < cnt; tok += 32 * ge.kw / kUnit) {
-        const int at4 = ((tok >> 3) * 32 + (j & 7) * 4 + ((tok & 7) >> 1)) * 4 + (tok & 1);
+        const int at4 = ((j & 7) * 4 + (tok >> 1)) * 4 + (tok & 1);
         float r0 = 0.f, r1 = 0.f;
         for (int w = 0; w < ge.kw; ++w) {
-          r0 += rf[at4 + w * NT * 128 + (ACT ? 0 : (j >> 3) * 2)];
-          if constexpr (ACT) r1 += rf[at4 + w * NT * 128 + 2];
+          r0 += rf[at4 + w * 128 + (ACT ? 0 : (j >> 3) * 2)];
+          if constexpr (ACT) r1 += rf[at4 + w * 128 + 2];
         }
         p.y[static_cast<long long>(off + tok) * p.ldy + nn] = from_f32<TYPE>(ACT ? silu_fast(r0) * r1 : r0);
       }
@@ -609,13 +595,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) grouped_few_kernel(const __gri
   }
 }
 
-template <int TYPE, int ACT, int NT>
+template <int TYPE, int ACT>
 cudaError_t launch_few(const GroupedParams& p, int dev, int sms, cudaStream_t s) {
-  constexpr int kRed = kFewWarps * NT * 512;
+  constexpr int kRed = kFewWarps * 512;
   constexpr int kStages = (226 * 1024 - static_cast<int>(sizeof(FewTab)) - 1024 - kRed) / kFewStage;
   constexpr int kSmem = kStages * kFewStage + kRed + 1024;
   static_assert(kStages >= 2 && kStages <= kFewMaxStages, "stages");
-  cudaError_t e = allow_smem_once<grouped_few_kernel<TYPE, ACT, NT>>(dev, kSmem);
+  cudaError_t e = allow_smem_once<grouped_few_kernel<TYPE, ACT>>(dev, kSmem);
   if (e != cudaSuccess) return e;
   FewParams fp;
   fp.g = p;
@@ -630,7 +616,7 @@ cudaError_t launch_few(const GroupedParams& p, int dev, int sms, cudaStream_t s)
   if (!(fp.blocks ? encode_16bit_blocks(&fp.tm, p.w, TYPE == kTBf16, rows, p.K, p.K, box, 2 * fp.kw)
                   : encode_16bit(&fp.tm, p.w, TYPE == kTBf16, rows, p.K, p.K, box)))
     return cudaErrorInvalidValue;
-  return launch_op(grouped_few_kernel<TYPE, ACT, NT>, dim3(sms), kFewThreads, kSmem, s, fp);
+  return launch_op(grouped_few_kernel<TYPE, ACT>, dim3(sms), kFewThreads, kSmem, s, fp);
 }
 
 template <int TYPE, int ACT>
@@ -638,11 +624,7 @@ cudaError_t launch_type(const GroupedParams& p, cudaStream_t s) {
   int dev, sms;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  if (p.P <= kFewRows) {
-    if (p.P <= 8) return launch_few<TYPE, ACT, 1>(p, dev, sms, s);
-    if (p.P <= 32) return launch_few<TYPE, ACT, 4>(p, dev, sms, s);
-    return launch_few<TYPE, ACT, 8>(p, dev, sms, s);
-  }
+  if (p.P <= kFewRows) return launch_few<TYPE, ACT>(p, dev, sms, s);
   const long long mean = p.P / p.E;
   const bool ga = p.row_of != nullptr;
   if (mean <= 64) return ga ? launch_mma<TYPE, ACT, 64, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 64, false>(p, dev, sms, s);

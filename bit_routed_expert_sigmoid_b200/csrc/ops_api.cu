@@ -15,6 +15,7 @@ constexpr int kMaxQ4Tokens = 65536;              // chunks of at least 8 tokens 
 constexpr int kMaxOpGroups = 1024;
 constexpr int kMaxOpTopK = 64;
 constexpr long long kMaxOpPairs = 1ll << 22;
+constexpr int kMaxCombineH = 1 << 23;            // blocks of 256 columns are a grid dimension
 constexpr int kMaxNormH = 32768;
 
 flint_status status_of(cudaError_t e) { return e == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA; }
@@ -34,7 +35,7 @@ flint_status flint_q4_linear(int fmt, int N, int K, int rotated, const void* cod
   const bool i4 = fmt == FLINT_W_INT4_G128_FWHT128;
   if (N < 1 || K < 1 || K % (i4 ? 128 : 16) != 0 || T < 0) return FLINT_ERR_INVALID_ARG;
   // byte offsets inside the rows of one CTA (at least 1/1024 of them) are 32 bits wide
-  if (K > kMaxOpK || T > kMaxQ4Tokens || static_cast<long long>(N) * K > (1ll << 37)) return FLINT_ERR_UNSUPPORTED;
+  if (K > kMaxOpK || T > kMaxQ4Tokens || N > (1 << 30) || static_cast<long long>(N) * K > (1ll << 37)) return FLINT_ERR_UNSUPPORTED;
   if ((rotated != 0 && rotated != 1) || (rotated && !i4) || !is_16bit(type)) return FLINT_ERR_INVALID_ARG;
   if (ldx < K || ldx % 8 != 0 || ldy < N) return FLINT_ERR_INVALID_ARG;
   if (T == 0) return FLINT_OK;
@@ -66,8 +67,8 @@ flint_status flint_grouped_linear(int E, int N, int K, int act, int type, const 
                                   long long ldy, void* stream) {
   if (E < 1 || N < 1 || K < 1 || K % 8 != 0 || P < 0 || x_rows < 0 || row_div < 1) return FLINT_ERR_INVALID_ARG;
   if (E > kMaxOpGroups || K > kMaxOpK || static_cast<long long>(E) * N > 0x7FFFFFFFll) return FLINT_ERR_UNSUPPORTED;
-  // tiles of 64 outputs x 64 rows are counted in 32 bits
-  if ((static_cast<long long>(N) / 64 + 1) * (P / 64 + static_cast<long long>(E)) > 0x7FFFFFFFll) return FLINT_ERR_UNSUPPORTED;
+  // tiles of 64 outputs x 64 rows are counted in 32 bits, whatever the offsets hold
+  if ((static_cast<long long>(N) / 64 + 1) * E > 0x7FFFFFFFll / (P / 64 + 1)) return FLINT_ERR_UNSUPPORTED;
   if ((act != FLINT_ACT_NONE && act != FLINT_ACT_SWIGLU) || !is_16bit(type)) return FLINT_ERR_INVALID_ARG;
   if (act == FLINT_ACT_SWIGLU && N % 2 != 0) return FLINT_ERR_INVALID_ARG;
   if (ldx < K || ldx % 8 != 0 || ldy < (act == FLINT_ACT_SWIGLU ? N / 2 : N)) return FLINT_ERR_INVALID_ARG;
@@ -109,7 +110,7 @@ flint_status flint_expert_combine(const void* o, long long ldo, int P, const int
                                   int H, float scale, const void* addend, long long lda, int type, void* y,
                                   long long ldy, void* stream) {
   if (T < 0 || P < 0 || top_k < 1 || H < 1 || !is_16bit(type)) return FLINT_ERR_INVALID_ARG;
-  if (top_k > kMaxOpTopK) return FLINT_ERR_UNSUPPORTED;
+  if (top_k > kMaxOpTopK || H > kMaxCombineH) return FLINT_ERR_UNSUPPORTED;
   if (ldo < H || ldy < H || (addend && lda < H)) return FLINT_ERR_INVALID_ARG;
   if (T == 0) return FLINT_OK;
   if ((P > 0 && !aligned_to(o, 2)) || !aligned_to(inv, 4) || !aligned_to(w, 4) || !opt_aligned(addend, 2) ||

@@ -26,7 +26,6 @@ constexpr int kQ4Warps = kQ4Threads / 32;
 // (token, segment) pairs up to which each CTA builds the operand itself: 8 per warp would take 5 us, the separate kernel
 // puts off the first product by 2.5 us.
 constexpr int kQ4Inline = 64;
-constexpr int kQ4InlineBytes = 40 * 1024;
 
 // d += A B on the integer tensor cores (m16n8k32): A s8, B s8 or u8
 template <bool SIGNED_B>
@@ -108,7 +107,9 @@ struct AFrag<kLimbs> {
 // x and for the scales each.
 constexpr int kRingThreads = kQ4Threads + 32;
 constexpr int kRingMaxStages = 8;
-constexpr int kQ4Split = 8;                      // warps of a team: two teams of 8 use a stage's x twice
+// Warps of a team at most: 8, two teams sharing a stage's x (8192 x 8192, T = 8: 15.4 us; 4 or 16 warps 18.0, 16.3),
+// but all 16 where a CTA has one block of rows (2048 x 2048, T = 8: 5.3 us against 6.4).
+constexpr int kQ4Split = 8;
 constexpr int kQ4ScaleBytes = 72 * 1024;         // scales kept in shared memory at most
 
 struct RingParams {
@@ -414,9 +415,10 @@ cudaError_t launch_rows(const Q4Params& p, int dev, int sms, int kw, cudaStream_
 template <int AR, int TYPE, bool TMA, bool INLINE>
 cudaError_t launch_ring(const Q4Params& p, int dev, int sms, cudaStream_t s) {
   const int segs = (p.K + 127) / 128;
+  const int blocks = ((p.N + sms - 1) / sms + 15) / 16, split = blocks == 1 ? kQ4Warps : kQ4Split;
   int kw = 1;
-  while (kw < segs && kw < kQ4Split) kw *= 2;
-  const int blocks = ((p.N + sms - 1) / sms + 15) / 16, teams = kQ4Warps / kw;
+  while (kw < segs && kw < split) kw *= 2;
+  const int teams = kQ4Warps / kw;
   if (blocks <= teams) return launch_rows<AR, TYPE, 1, TMA, INLINE>(p, dev, sms, kw, s);
   return launch_rows<AR, TYPE, 2, TMA, INLINE>(p, dev, sms, kw, s);
 }
@@ -450,7 +452,7 @@ cudaError_t read_q4_error(unsigned* out) {
 
 size_t q4_workspace_bytes(int K, int T) {
   const int segs = (K + 127) / 128;
-  if (T <= 8 && T * segs <= kQ4Inline && q4_operand_bytes(T, segs) <= kQ4InlineBytes) return 0;
+  if (T <= 8 && T * segs <= kQ4Inline) return 0;
   return q4_operand_bytes(T, segs);
 }
 

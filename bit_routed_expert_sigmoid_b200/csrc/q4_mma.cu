@@ -12,6 +12,8 @@
 // of codes that are no multiple of 16 bytes (K % 32 = 16) are read by the decoding warps themselves.
 // (With the tokens on the M side every MMA reads 128 operand rows from shared memory, 32 KB per segment whatever T is:
 // that took 46 us for 8192 x 8192.)
+#include <limits.h>
+
 #include "kernels.cuh"
 #include "ops.cuh"
 #include "q4_operand.cuh"
@@ -24,17 +26,19 @@ __device__ unsigned g_ops_error_q4mma;           // timeout bits of bounded wait
 
 namespace {
 
-constexpr int kMmTeams = 4;                      // decoding teams of four warps
+constexpr int kMmTeams = 2;                      // decoding teams of four warps
 constexpr int kMmSums = 4 + 4 * kMmTeams;        // first of the 8 summing warps; before: copies 2, MMA 2, decoding
 constexpr int kMmThreads = 32 * (kMmSums + 8);
 constexpr int kMmTokens = 64;                    // tokens at a time at most
 constexpr int kMmChunk = 4;                      // segments of codes per stage
 constexpr int kMmA = 4;                          // decoded segments in tensor memory (64 columns each)
 constexpr int kMmD = 4;                          // accumulators (64 columns each)
-// Segments of factors kept for the sums: the MMA is at most kMmD segments ahead of them, copies at most SB <= 3 pairs
+// Segments of factors kept for the sums: the MMA is at most kMmD segments ahead of them, copies at most kMmPairStages pairs
 // ahead of the MMA.
 constexpr int kMmRing = 16;
-constexpr int kMmMaxStages = 4;
+// Stages of codes (one where large tiles leave no room for two; up to four: 21.6 us against 21.1 for 8192 x 8192 at
+// T = 16) and of the operand.
+constexpr int kMmCodeStages = 2, kMmPairStages = 3;
 constexpr int kMmMaxSplit = 8;                   // CTAs per tile (portable cluster size)
 constexpr int kMmScaleBytes = 32 * 1024;
 
@@ -46,13 +50,13 @@ struct MmParams {
   int R;                                         // rows of a tile
   int split, range;                              // CTAs per tile, segments of each
   int TB;                                        // tokens at a time, a multiple of 8
-  int SC, SB;                                    // stages of codes and of the operand
+  int SC;                                        // stages of codes
   int boxed;
   int scale_row;                                 // bytes of a row's scales kept in shared memory, 0: none
 };
 
 struct MmBars {
-  uint64_t c_full[kMmMaxStages], c_empty[kMmMaxStages], b_full[kMmMaxStages], b_empty[kMmMaxStages];
+  uint64_t c_full[kMmCodeStages], c_empty[kMmCodeStages], b_full[kMmPairStages], b_empty[kMmPairStages];
   uint64_t a_full[kMmA], a_empty[kMmA], d_full[kMmD], d_empty[kMmD], done[2], scales;
   uint32_t tmem;
   int abort;
@@ -94,19 +98,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
   const int seg0 = rank * mp.range, segs = max(min(mp.range, all_segs - seg0), 0);     // this CTA's segments
   const int pairs = (segs + 1) / 2, chunks = (segs + kMmChunk - 1) / kMmChunk;
   const int R = mp.R, TB = mp.TB, row0 = tile * R, rows = min(R, p.N - row0);
-  const int b_stage = TB * 512, c_stage = mm_code_stage(R);
+  const int b_stage = TB * 512, c_stage = TMA ? mm_code_stage(R) : 0;
   const int t0 = blockIdx.y * TB, N16 = (TB + 15) & ~15;
   uint8_t* sm_b = align1024(smem_raw);
-  uint8_t* sm_c = sm_b + mp.SB * b_stage;
+  uint8_t* sm_c = sm_b + kMmPairStages * b_stage;
   uint8_t* sm_s = sm_c + mp.SC * c_stage;
   volatile int* abort = &bb.abort;
   unsigned* err = &g_ops_error_q4mma;
   const long long scale_row = kI4 ? p.K >> 6 : p.K >> 4;         // bytes
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMmMaxStages; ++i) {
+    for (int i = 0; i < kMmCodeStages; ++i) {
       mbar_init(&bb.c_full[i], 1);
       mbar_init(&bb.c_empty[i], 4 * kMmTeams);
+    }
+    for (int i = 0; i < kMmPairStages; ++i) {
       mbar_init(&bb.b_full[i], 1);
       mbar_init(&bb.b_empty[i], 2);
     }
@@ -173,14 +179,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
       const float* fac = reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.workspace) + q4_rows_factors(p.T, all_segs)) + t0;
       int it = 0;
       for (; it < pairs; ++it) {
-        const int slot = it % mp.SB, seg = 2 * it, n = min(2, segs - seg);
-        if (it >= mp.SB && !pf_wait(&bb.b_empty[slot], ((it / mp.SB) - 1) & 1, abort, err)) break;
+        const int slot = it % kMmPairStages, seg = 2 * it, n = min(2, segs - seg);
+        if (it >= kMmPairStages && !pf_wait(&bb.b_empty[slot], ((it / kMmPairStages) - 1) & 1, abort, err)) break;
         mbar_arrive_expect_tx(&bb.b_full[slot], b_stage + n * fbytes);
         tma_3d(sm_b + slot * b_stage, &mp.tm_x, 0, t0, 2 * (seg0 + seg), &bb.b_full[slot]);
         for (int j = 0; j < n; ++j)
           bulk_g2s(s_factor[(seg + j) % kMmRing], fac + static_cast<size_t>(seg0 + seg + j) * tpad, fbytes, &bb.b_full[slot]);
       }
-      for (int j = max(it - mp.SB, 0); j < it; ++j) mbar_wait_bounded(&bb.b_full[j % mp.SB], (j / mp.SB) & 1, 1000000);
+      for (int j = max(it - kMmPairStages, 0); j < it; ++j) mbar_wait_bounded(&bb.b_full[j % kMmPairStages], (j / kMmPairStages) & 1, 1000000);
     }
   } else if (warp < 4) {
     // ---- MMA: segments of one parity. kMmA and kMmD are even, so that a place of either belongs to one warp; both
@@ -188,8 +194,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     const int w = warp - 2;
     const uint32_t idesc = idesc_m128(N16, false);
     for (int it = 0; it < pairs; ++it) {
-      const int seg = 2 * it + w, sb = it % mp.SB, sa = seg % kMmA, sd = seg % kMmD;
-      if (!pf_wait_all(&bb.b_full[sb], (it / mp.SB) & 1, abort, err)) break;
+      const int seg = 2 * it + w, sb = it % kMmPairStages, sa = seg % kMmA, sd = seg % kMmD;
+      if (!pf_wait_all(&bb.b_full[sb], (it / kMmPairStages) & 1, abort, err)) break;
       if (seg < segs) {
         if (seg >= kMmD && !pf_wait_all(&bb.d_empty[sd], ((seg / kMmD) - 1) & 1, abort, err)) break;
         if (!pf_wait_all(&bb.a_full[sa], (seg / kMmA) & 1, abort, err)) break;
@@ -401,24 +407,24 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
   const int segs = (p.K + 127) / 128;
   MmParams mp;
   mp.q = p;
-  // Tiles and splits: of the splits for which the tiles (as many as the SMs then hold, of at most 128 rows) make one
-  // wave, the one with the least work per CTA, a segment costing about as much as 64 rows' decoding whatever its rows;
-  // more rows than one wave holds go unsplit.
+  // Tiles and splits: a CTA takes 0.4 us per segment (NVFP4 0.6), whatever the height of its tile. Of the splits for which
+  // the tiles (as many as the SMs then hold, of at most 128 rows) make one wave, the one with the fewest segments per CTA
+  // (2048 x 2048, T = 9: 12.6, 10.0, 9.2 and 8.5 us split 1, 2, 3 and 4 ways); more rows than one wave holds go unsplit.
   mp.split = 1;
   mp.R = 128;
-  long long best = -1;
+  mp.range = INT_MAX;
   for (int k = 1; k <= kMmMaxSplit && k <= segs; ++k) {
     const int tiles = clusters_of(dev, sms, k), R = tiles > 0 ? (p.N + tiles - 1) / tiles : 129;
     if (R > 128) continue;
-    const long long cost = static_cast<long long>(((segs + k - 1) / k + 1) & ~1) * (64 + R) + 150 * k;
-    if (best < 0 || cost < best) {
-      best = cost;
+    int range = (segs + k - 1) / k;
+    if (TMA) range = (range + 1) & ~1;           // it starts with a 256-code block
+    if (range < mp.range) {
+      mp.range = range;
       mp.split = k;
       mp.R = R < 8 ? 8 : R;
     }
   }
-  mp.range = (segs + mp.split - 1) / mp.split;
-  if (TMA) mp.range = (mp.range + 1) & ~1;       // a range starts with a 256-code block
+  if (mp.range > segs) mp.range = TMA ? (segs + 1) & ~1 : segs;
   const int tiles = (p.N + mp.R - 1) / mp.R;
   const int token_chunks = (p.T + kMmTokens - 1) / kMmTokens;
   mp.TB = ((p.T + token_chunks - 1) / token_chunks + 7) & ~7;
@@ -431,15 +437,14 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
                      : 0;
   const int b_stage = mp.TB * 512, c_stage = TMA ? mm_code_stage(mp.R) : 0;
   const int fixed = 1024 + mp.R * mp.scale_row;
-  mp.SB = 3;
-  mp.SC = TMA ? (kMost - fixed - mp.SB * b_stage) / c_stage : 1;
-  if (mp.SC > kMmMaxStages) mp.SC = kMmMaxStages;
+  mp.SC = TMA ? (kMost - fixed - kMmPairStages * b_stage) / c_stage : 1;
+  if (mp.SC > kMmCodeStages) mp.SC = kMmCodeStages;
   if (mp.SC < 1) return cudaErrorInvalidConfiguration;
-  int smem = fixed + mp.SB * b_stage + mp.SC * c_stage;
+  int smem = fixed + kMmPairStages * b_stage + mp.SC * c_stage;
   const int parts = 1024 + mp.split * ((mp.TB + mp.split - 1) / mp.split) * 512;
   if (smem < parts) smem = parts;
   // the MMA reads N16 rows of the operand's last block, up to 8 more than there are
-  if (smem < 1024 + mp.SB * b_stage + 1024) smem = 1024 + mp.SB * b_stage + 1024;
+  if (smem < 1024 + kMmPairStages * b_stage + 1024) smem = 1024 + kMmPairStages * b_stage + 1024;
   if (smem > kMost) return cudaErrorInvalidConfiguration;
   if (TMA && !(mp.boxed ? encode_words_blocks(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R, kMmChunk / 2)
                         : encode_words(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R)))

@@ -21,8 +21,7 @@ enum Arith : int { kF16Int4, kF16Nvfp4, kLimbs };
 
 // A (token, segment) is four chunks of 16 bytes for each of the four lanes q that read it, K = 32 q .. 32 q + 31. fp16:
 // chunk i holds K = 32 q + 8 i .. + 7 in the order of the decoded pairs (int4 0,4,1,5,2,6,3,7; NVFP4 0,1,2,6,4,5,3,7);
-// limbs: chunk 2 limb +
-// (i >> 1) holds at 8 (i & 1) the bytes of K = 32 q + 8 i + 0, 2, 4, 6 and of + 1, 3, 5, 7.
+// limbs: chunk 2 limb + (i >> 1) holds at 8 (i & 1) the bytes of K = 32 q + 8 i + 0, 2, 4, 6 and of + 1, 3, 5, 7.
 //   kTokens  [segment][token][chunk][q], then the inverse factor, kTokenBytes each
 //   kRows    [token][segment][q][chunk]: K-major rows; then the factors [segment][tokens rounded up to 4]
 // kTokens is for up to 8 tokens (q4_linear.cu), kRows for more (q4_mma.cu).

@@ -2,7 +2,7 @@
 
 As in `layer`, PyTorch supplies device memory and streams only; every step runs in the library's CUDA
 kernels. Shapes, types and strides are checked here (ValueError) or by the C entry points (FlintError).
-Outputs that are not given are allocated. Work goes to `stream` (default: the current stream of the
+Outputs that are not given are allocated; no gradients are recorded. Work goes to `stream` (default: the current stream of the
 inputs' device); an input written on another stream must have been ordered before it by the caller.
 
 The smallest calls take a few microseconds on the device, so the common path (tensors of the current
@@ -18,6 +18,7 @@ from . import binding as B
 _TYPES = {torch.bfloat16: B.FLINT_T_BF16, torch.float16: B.FLINT_T_F16}
 _FORMATS = {"int4": B.FLINT_W_INT4_G128_FWHT128, "nvfp4": B.FLINT_W_NVFP4}
 _ACTS = {None: B.FLINT_ACT_NONE, "none": B.FLINT_ACT_NONE, "swiglu": B.FLINT_ACT_SWIGLU}
+_SCALES = {"int4": (torch.bfloat16,), "nvfp4": (torch.float8_e4m3fn, torch.uint8)}
 _GATES = {None: B.FLINT_GATE_NONE, "none": B.FLINT_GATE_NONE, "sigmoid": B.FLINT_GATE_SIGMOID}
 
 _current_device = torch.cuda.current_device
@@ -86,7 +87,7 @@ def q4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tscale
     group = 128 if fmt == "int4" else 16
     if codes.dtype != torch.uint8 or codes.shape != (N, K // 2) or K % 2 or not codes.is_contiguous():
         raise ValueError("codes must be contiguous u8 [N][K/2]")
-    if scales.shape != (N, K // group) or scales.element_size() != (2 if group == 128 else 1) or not scales.is_contiguous():
+    if scales.shape != (N, K // group) or scales.dtype not in _SCALES[fmt] or not scales.is_contiguous():
         raise ValueError("scales must be contiguous bf16 [N][K/128] (int4) or E4M3 [N][K/16] (nvfp4)")
     if tscale is not None and (tscale.dtype != torch.float32 or tscale.numel() != 1):
         raise ValueError("tscale must be f32 [1]")

@@ -7,8 +7,8 @@
  * The conventions of flint_moe.h hold: device pointers owned by the caller, work enqueued on `stream` and
  * never waited for, nothing allocated, bad arguments refused before anything is launched. Every function
  * is stateless (no handle), so calls on different streams may overlap as long as they share no workspace,
- * and all of them can be captured into CUDA graphs. The current device must be the stream's. Leading dimensions (ld*) count
- * elements between rows. Outputs must not overlap inputs unless a function says so. Sums run in fp32 in a
+ * and all of them can be captured into CUDA graphs. The current device must be the stream's. Leading dimensions (ld*)
+ * count elements between rows. Outputs must not overlap inputs unless a function says so. Sums run in fp32 in a
  * fixed order: the same call gives the same bits. Results are rounded once, to the output's type.
  */
 #ifndef FLINT_OPS_H
@@ -33,8 +33,11 @@ extern "C" {
  *   fmt FLINT_W_NVFP4: codes u8 [N][K/2], scales E4M3 [N][K/16], K a multiple of 16; rotated = 0.
  * tscale f32 [1] (device) multiplies the sum: required for NVFP4, optional (NULL = 1) for int4.
  * x [T][K] and y [T][N] are of `type` (BF16 or F16). codes and x are 16-byte aligned and ldx is a multiple of
- * 8; y, ldy need no alignment beyond their element's. K, T <= 65536. Made for few tokens (T <= 64); larger T run
- * in chunks that read the weights again. T = 0 is a no-op.
+ * 8; y, ldy need no alignment beyond their element's. K, T <= 65536, N <= 2^30, N * K <= 2^37. Made for few tokens
+ * (T <= 64): larger T run in chunks that read the weights again. T = 0 is a no-op.
+ * Rounding before the sums: rotated activations, per (token, 128-segment), to 16-bit fixed point of the segment's
+ * largest value (T <= 8) or, scaled by a power of two, to fp16 (T > 8). Unrotated ones, and the codes times NVFP4's
+ * block scales, enter exactly, but for activations below 2^-29 of their segment's largest.
  * workspace: flint_q4_linear_workspace_size(K, T) bytes of device memory (the activations as the kernel's operand),
  * 256-byte aligned, in use until the call's work is done; may be NULL when that size is 0, as it is for the smallest
  * calls. The size is 0 for invalid arguments too. */
@@ -54,8 +57,8 @@ flint_status flint_q4_linear(int fmt, int N, int K, int rotated, const void* cod
  * a group that ends before it begins is empty. Rows of y at or behind offsets[E] are left as they were.
  * row_of int32 [P] (device) or NULL; with the permutation of flint_expert_permute or flint_moe_routing
  * (perm[p] = token * top_k + slot), row_div = top_k makes r(p) the token. r(p) outside [0, x_rows) is clamped.
- * 1 <= E <= 1024, K a multiple of 8, K <= 65536, E * N < 2^31, (N/64 + 1) (P/64 + E) < 2^31; w and x are 16-byte aligned, ldx is a multiple
- * of 8; y needs no alignment beyond its element's. P = 0 is a no-op. */
+ * 1 <= E <= 1024, K a multiple of 8, K <= 65536, E * N < 2^31, (N/64 + 1) E (P/64 + 1) < 2^31; w and x are 16-byte
+ * aligned, ldx is a multiple of 8; y needs no alignment beyond its element's. P = 0 is a no-op. */
 flint_status flint_grouped_linear(int E, int N, int K, int act, int type, const void* w, const void* x, long long ldx,
                                   int x_rows, const int* row_of, int row_div, const int* offsets, int P, void* y,
                                   long long ldy, void* stream);
@@ -71,7 +74,7 @@ flint_status flint_expert_permute(const int* ids, int T, int top_k, int E, int* 
 
 /* y[t] = scale * sum_k w[t][k] o[inv[t][k]] + addend[t]  (slot order; slots with inv outside [0, P) are skipped,
  * whatever their weight). o [P][H], addend [T][H] (NULL: none) and y [T][H] of `type` (BF16 or F16); inv int32,
- * w f32 [T][top_k]. addend may be y. 1 <= top_k <= 64, H >= 1. T = 0 is a no-op. */
+ * w f32 [T][top_k]. addend may be y. 1 <= top_k <= 64, 1 <= H <= 2^23. T = 0 is a no-op. */
 flint_status flint_expert_combine(const void* o, long long ldo, int P, const int* inv, const float* w, int T, int top_k,
                                   int H, float scale, const void* addend, long long lda, int type, void* y,
                                   long long ldy, void* stream);
@@ -106,7 +109,7 @@ typedef struct flint_norm_args {
 flint_status flint_block_norm(const flint_norm_args* args, void* stream);
 
 /* Reads and clears the operators' error word of the current device: 0, or the timeout bit (4) when a bounded wait
- * inside a kernel of flint_grouped_linear gave up since the last call (its output is then incomplete). Waits for
+ * inside a kernel of flint_q4_linear or flint_grouped_linear gave up since the last call (its output is then incomplete). Waits for
  * the device. */
 flint_status flint_ops_error_word(unsigned* out);
 

@@ -139,6 +139,58 @@ def test_q4_extreme_activations_stay_in_their_row():
             assert torch.equal(y[3] > 0, (scales[:, 0] > 0))
 
 
+@pytest.mark.parametrize("fmt,N,K,T", [("int4", 20001, 128, 3), ("int4", 20001, 256, 11), ("nvfp4", 40003, 32, 8), ("nvfp4", 19001, 64, 17),
+                                       ("int4", 3, 65536, 1), ("int4", 24, 65536, 8), ("int4", 9, 65536, 12), ("nvfp4", 5, 65536, 70),
+                                       ("nvfp4", 6, 65520, 5), ("nvfp4", 6, 65520, 9), ("int4", 7, 128, 700)])
+def test_q4_at_the_ends_of_its_range(fmt, N, K, T):
+    # more rows than one wave of full tiles, the longest K on few rows, many chunks of tokens
+    x, codes, scales, ts = q4_case(fmt, N, K, T, torch.bfloat16, N + K + T)
+    y = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=fmt == "int4")
+    ref, slack = q4_reference(x, codes, scales, ts, fmt, fmt == "int4")
+    close(y, ref, torch.bfloat16, slack, 2.0 ** -11 if fmt == "int4" else 0.0)
+
+
+@pytest.mark.parametrize("T", [1, 5, 8, 20])
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
+def test_q4_scales_at_any_address(fmt, T):
+    # scales that start inside a buffer, one element behind a 16-byte boundary: the same bits as aligned ones
+    x, codes, scales, ts = q4_case(fmt, 130, 1024, T, torch.bfloat16, T)
+    raw = torch.empty(scales.numel() + 1, dtype=scales.dtype, device="cuda")
+    moved = raw[1:].view(scales.shape)
+    moved.copy_(scales)
+    assert moved.data_ptr() % 16 != 0
+    want = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=False)
+    assert torch.equal(ops.q4_linear(x, codes, moved, ts, fmt=fmt, rotated=False), want)
+
+
+@pytest.mark.parametrize("T", [2, 8, 24])
+def test_q4_reads_weights_written_just_before(T):
+    # codes, scales and activations rewritten on the stream before every call, in a graph as well: each call sees its own
+    N, K = 2048, 1024
+    cases = [q4_case("int4", N, K, T, torch.bfloat16, s) for s in range(4)]
+    want = [ops.q4_linear(x, c, s) for x, c, s, _ in cases]
+    torch.cuda.synchronize()
+    x, c, s = (torch.empty_like(t) for t in cases[0][:3])
+
+    def steps():
+        out = []
+        for a, b, d, _ in cases:
+            s.copy_(d), c.copy_(b), x.copy_(a)
+            out.append(ops.q4_linear(x, c, s))
+        return out
+    for got in (steps(), steps()):
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = steps()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(out, want):
+            assert torch.equal(u, v)
+
+
 def test_q4_writes_only_its_columns_and_repeats_bit_for_bit():
     x, codes, scales, _ = q4_case("int4", 77, 384, 11, torch.float16, 6)
     buf = torch.full((11, 100), 7.0, dtype=torch.float16, device="cuda")

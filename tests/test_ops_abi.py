@@ -36,6 +36,8 @@ def test_q4_linear_refuses(kw):
 def test_q4_linear_limits_and_no_op():
     assert _status("flint_q4_linear", Q4, K=65536 + 128, ldx=65536 + 128) == UNSUPPORTED
     assert _status("flint_q4_linear", Q4, T=65537) == UNSUPPORTED
+    assert _status("flint_q4_linear", Q4, N=(1 << 30) + 1, ldy=1 << 31, K=128, ldx=128) == UNSUPPORTED
+    assert _status("flint_q4_linear", Q4, N=1 << 26, ldy=1 << 26, K=4096, ldx=4096) == UNSUPPORTED
     big = dict(T=64, K=4096, ldx=4096)                     # needs a workspace: missing, misaligned, too small
     need = B.flint_q4_linear_workspace_size(4096, 64)
     assert need > 0 and B.flint_q4_linear_workspace_size(256, 4) == B.flint_q4_linear_workspace_size(0, 64) == 0
@@ -59,7 +61,8 @@ def test_grouped_linear_refuses(kw):
 
 def test_grouped_linear_limits_and_no_op():
     for kw in (dict(E=1025), dict(K=65544, ldx=65544), dict(E=1024, N=1 << 21, ldy=1 << 21),
-               dict(E=1, N=1 << 20, ldy=1 << 20, P=1 << 30, x_rows=1 << 30)):
+               dict(E=1, N=1 << 20, ldy=1 << 20, P=1 << 30, x_rows=1 << 30),
+               dict(E=1024, N=32768, ldy=32768, P=1 << 20, x_rows=1 << 20)):     # tiles of groups that all overlap
         assert _status("flint_grouped_linear", GR, **kw) == UNSUPPORTED
     assert _status("flint_grouped_linear", GR, P=0, x_rows=0, w=0, x=0, y=0, offsets=0) == OK
 
@@ -91,6 +94,8 @@ def test_combine_refuses(kw):
 
 def test_combine_limits_and_no_op():
     assert _status("flint_expert_combine", CO, top_k=65) == UNSUPPORTED
+    big = (1 << 23) + 8
+    assert _status("flint_expert_combine", CO, H=big, ldo=big, lda=big, ldy=big) == UNSUPPORTED
     assert _status("flint_expert_combine", CO, T=0, o=0, inv=0, w=0, y=0, addend=0) == OK
 
 
@@ -138,3 +143,15 @@ def test_wrappers_refuse_cpu_tensors_and_bad_shapes():
                  lambda: ops.block_norm(x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_wrappers_refuse_other_scale_types(monkeypatch):
+    # the checks run before anything touches a device: let CPU tensors through to them
+    monkeypatch.setattr(ops, "_elsewhere", lambda device, stream: False)
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    codes = torch.zeros((4, 64), dtype=torch.uint8)
+    for fmt, scales in (("int4", torch.zeros((4, 1), dtype=torch.float16)), ("int4", torch.zeros((4, 1), dtype=torch.int16)),
+                        ("nvfp4", torch.zeros((4, 8), dtype=torch.float8_e5m2)), ("nvfp4", torch.zeros((4, 8), dtype=torch.int8)),
+                        ("int4", torch.zeros((4, 2), dtype=torch.bfloat16))):
+        with pytest.raises(ValueError, match="scales"):
+            ops.q4_linear(x, codes, scales, torch.ones(1), fmt=fmt, rotated=False)
