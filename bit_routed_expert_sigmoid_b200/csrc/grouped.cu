@@ -7,7 +7,8 @@
 // order, as TMA boxes; rows taken through row_of by four warps with 16-byte cp.async, so no gathered copy of x is
 // ever written (TMA's gather4 measured ~70 cycles per four 128-byte rows: 4096^3 took 602 us with it). With few
 // rows per expert it is bound by streaming the weights once; with many, by the tensor cores.
-// grouped_few_kernel serves decode (P <= kFewRows): see there.
+// grouped_few_kernel serves decode (P <= kFewRows): see there. 256 experts, gate|up 1024 x 2048: 12288 rows 160 us, 192
+// rows 91 (HBM 167 and 87 with a cold L2), 24 rows 21.4 (14.9); one group of 4096^3 105 us (tensor cores 82).
 #include "kernels.cuh"
 #include "ops.cuh"
 #include "tc.cuh"
@@ -25,6 +26,9 @@ constexpr int kGrTabWarps = 8;                   // warps that build the tile ta
 constexpr int kGrGather = 128;
 constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
 constexpr int kGrSlab = 2 * 2 * 16 * 64 * 4;      // SwiGLU: two teams x (gate, up) x 16 columns x 64 rows, fp32
+// Rows up to which grouped_few_kernel is taken: 24 rows over 256 experts take 21.4 us there and 26.6 by the GEMM, 30 rows
+// 25.1 and 26.7, 60 rows 44 and 38. Groups of more than eight rows on average go to the GEMM, as their weights would be
+// read once per eight (28 rows of two experts, 4096 x 4096: 24.5 us and 20.4).
 constexpr int kFewRows = 32;
 
 // First row and number of rows of group e; offsets clamped to [0, P].
@@ -403,8 +407,8 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
 // SM, boxes of 8 KB and more over twice that.
 constexpr int kFewWarps = 16;                    // consumers; one more warp copies
 constexpr int kFewThreads = 32 * (kFewWarps + 1);
-// Warps of a team at most, each with 128 K of a stage: 8 (fewer idle teams in the last round: 24 rows over 256 experts
-// 24.9 us against 26.6, 60 rows 45.2 against 47.7), but 4 when a CTA has few units (6 rows 9.9 us against 10.9).
+// Warps of a team at most, each with 128 K of a stage: 8 (fewer idle teams in the last round: 12 rows over 256 experts
+// 14.7 us against 16.0, 30 rows 25.1 against 27.2), but 4 when a CTA has few units (6 rows 9.6 us against 10.7).
 constexpr int kFewSplit = 8;
 constexpr int kFewMaxStages = 8;
 
@@ -624,9 +628,11 @@ cudaError_t launch_type(const GroupedParams& p, cudaStream_t s) {
   int dev, sms;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  if (p.P <= kFewRows) return launch_few<TYPE, ACT>(p, dev, sms, s);
+  if (p.P <= kFewRows && (p.P <= 8 || p.P / 8 <= p.E)) return launch_few<TYPE, ACT>(p, dev, sms, s);
   const long long mean = p.P / p.E;
   const bool ga = p.row_of != nullptr;
+  // Rows of a tile by the mean group: 48 rows 161 us with 64, 178 with 128 (12288 rows over 256 experts); 82 rows 24.8, 24.1
+  // and 27.2 us with 64, 128 and 256 (5003 rows over 61 experts, uneven)
   if (mean <= 64) return ga ? launch_mma<TYPE, ACT, 64, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 64, false>(p, dev, sms, s);
   if (mean <= 128) return ga ? launch_mma<TYPE, ACT, 128, true>(p, dev, sms, s) : launch_mma<TYPE, ACT, 128, false>(p, dev, sms, s);
   // Two blocks where rows are gathered and the tiles then still fill the SMs: 16384 tokens over 256 experts, gate|up,
