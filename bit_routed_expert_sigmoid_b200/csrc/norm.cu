@@ -1,6 +1,6 @@
 // The residual step around a block (flint_block_norm): post-norm of the branch, gate, residual add and the
 // next block's pre-norm in one pass, every row read once and held in registers between the two reductions. Bound by HBM:
-// 8192 x 4096 bf16 with a gate per element moves 336 MB in 65.0 us (5.2 TB/s); 2048 x 2048 with an fp32 residual 9.1 us.
+// 8192 x 4096 bf16 with a gate per element moves 336 MB in 58.0 us (5.8 TB/s); 2048 x 2048 with an fp32 residual 9.2 us.
 #include "kernels.cuh"
 #include "ops.cuh"
 
@@ -104,6 +104,15 @@ __device__ __forceinline__ void load8_weight(const void* w, int w_f32, int v, in
   else widen8<TYPE>(load8<VEC>(static_cast<const uint16_t*>(w), v, H), out);
 }
 
+// 1 / (1 + e^-g) by the approximate base-2 exponential and reciprocal: within (|g| + 4) 2^-24 of itself, and 0 where e^-g passes
+// 2^126
+__device__ __forceinline__ float sigmoid_fast(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
 template <int VPT>
 constexpr int kMaxThreads = VPT == 1 ? 1024 : VPT == 8 ? 512 : 256;
 
@@ -155,9 +164,13 @@ __global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __gr
       if (p.gate) {
         float g[8];
         widen8<TYPE>(gr[v], g);
-        // the fast exponential and division are within a few units of fp32's last place
+        if (p.gate_act == 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] *= p.gate_act == 1 ? __fdividef(1.0f, 1.0f + __expf(-g[j])) : g[j];
+          for (int j = 0; j < 8; ++j) b[j] *= sigmoid_fast(g[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b[j] *= g[j];
+        }
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[v][j] = fmaf(p.branch_scale, b[j], p.res_scale * x[v][j]);
@@ -198,10 +211,14 @@ __global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __gr
   const float inv = 1.0f / sqrtf(block_sum(s, sum_pre) / static_cast<float>(H) + p.eps);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    float w[8];
-    if (p.pre_w) load8_weight<TYPE, VEC>(p.pre_w, p.w_f32, v, H, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[v][j] = x[v][j] * inv * (p.pre_w ? w[j] : 1.0f);
+    for (int j = 0; j < 8; ++j) x[v][j] *= inv;
+    if (p.pre_w) {
+      float w[8];
+      load8_weight<TYPE, VEC>(p.pre_w, p.w_f32, v, H, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] *= w[j];
+    }
     store8<TYPE, VEC>(p.z + t * p.ldz, v, H, x[v]);
   }
 }
@@ -209,14 +226,13 @@ __global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __gr
 template <int TYPE, bool RES_F32, bool VEC>
 cudaError_t launch_vpt(const NormParams& p, cudaStream_t s) {
   // Few rows: a thread per 8 columns, the shortest way through one row (4 x 2048: 2.3 us, 2.4 with two steps). Many rows:
-  // up to 4 steps per thread, so that the reductions cost fewer warps and more loads of more rows are in flight
-  // (8192 x 4096 with a gate per element: 65.0 us, 76.4 with one step).
+  // 4 steps per thread, so that the reductions cost fewer warps and more loads of more rows are in flight (8192 x 4096
+  // with a gate per element: 58.0 us, 63.4 with two steps, 76 with one).
   const int n8 = (p.H + 7) / 8;
-  const int vpt = n8 > 1024 ? 8 : p.T >= 1024 && n8 > 512 ? 4 : p.T >= 1024 && n8 > 256 ? 2 : 1;
+  const int vpt = n8 > 1024 ? 8 : p.T >= 1024 && n8 > 256 ? 4 : 1;
   const int threads = ((n8 + vpt - 1) / vpt + 31) / 32 * 32;
   switch (vpt) {
     case 1: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 1>, dim3(p.T), threads, 0, s, p);
-    case 2: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 2>, dim3(p.T), threads, 0, s, p);
     case 4: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 4>, dim3(p.T), threads, 0, s, p);
     default: return launch_op(block_norm_kernel<TYPE, RES_F32, VEC, 8>, dim3(p.T), threads, 0, s, p);
   }

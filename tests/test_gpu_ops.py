@@ -409,7 +409,7 @@ def test_combine_skips_dropped_rows_whatever_they_hold():
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("res32", [True, False])
-@pytest.mark.parametrize("T,H", [(1, 1), (4, 2048), (3, 65), (17, 512), (2, 8192), (5, 8200), (2, 20000), (9, 4095), (1, 32768)])
+@pytest.mark.parametrize("T,H", [(1, 1), (4, 2048), (3, 65), (17, 512), (2, 8192), (5, 8200), (2, 20000), (9, 4095), (1, 32768), (1030, 2056), (1025, 4095)])
 @pytest.mark.parametrize("mode", ["plain", "branch", "post", "gate_row", "gate_token"])
 def test_block_norm(T, H, mode, res32, dtype):
     g = torch.Generator().manual_seed(T + H)
