@@ -395,12 +395,12 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows (P <= kFewRows): bound by streaming the active groups' weights once. The weight rows of all active
-// groups are cut into units of 16 (SwiGLU: 8 gate rows and their 8 up rows) and spread evenly over one CTA per SM,
-// which a GEMM's 128-row tiles cannot do when a token has six experts. One thread keeps a ring of stages full: a
-// stage is up to 512 K of the units that the 16 other warps work on, in teams of four warps per unit (fewer when K is
-// short), one TMA box of 8 or 16 KB per unit (half unit with SwiGLU). A warp takes 128 K of a stage and multiplies
-// with mma.sync m16n8k16; any order of K serves as long as both operands have it, so a lane reads 8 neighbouring K at
+// Few rows (P <= kFewRows): bound by streaming the active groups' weights once. A group makes an entry per eight of its
+// rows (the MMA's columns; one entry, as a rule); the weight rows of all entries are cut into units of 16 (SwiGLU: 8 gate
+// rows and their 8 up rows) and spread evenly over one CTA per SM, which a GEMM's 128-row tiles cannot do when a token has
+// six experts. One thread keeps a ring of stages full: a stage is up to 1024 K of the units that the 16 other warps work
+// on, in teams of eight or four warps per unit (fewer when K is short), one TMA box of up to 32 KB per unit (half a unit
+// with SwiGLU). A warp takes 128 K of a stage and multiplies with mma.sync m16n8k16; any order of K serves as long as both operands have it, so a lane reads 8 neighbouring K at
 // a time and x comes straight from global memory, through L1. A team's partial sums meet in shared memory and are
 // added in warp order; teams do not wait for one another.
 // Small copies starve it: bulk copies of one row (1 or 4 KB) and boxes of 2 KB all streamed ~11 bytes per cycle and

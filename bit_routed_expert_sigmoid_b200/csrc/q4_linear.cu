@@ -3,9 +3,9 @@
 //
 // Up to 8 tokens (this file; more: q4_mma.cu) it is bound by streaming the weights once, and close behind by the
 // instructions that decode them: 8192 x 8192 int4 takes 15.4 us at T = 8 and 12.7 at T = 1 (HBM 5.3; a launch that only
-// reads the codes 8.3), NVFP4 22.8; T = 9 takes 20.1 in the other file. The rows of W are divided evenly over one CTA per SM (not in units of a tile); the 16
-// warps of a CTA split K: a warp takes a 128-segment of one or two blocks of up to 16 rows at a time, as fragments of
-// mma.sync. A fragment's K order is free as long as x has the same: a lane's 16 bytes are 32 neighbouring K of one row.
+// reads the codes 8.3), NVFP4 22.8; T = 9 takes 20.1 in the other file.
+// The rows of W are divided evenly over one CTA per SM (not in units of a tile); the 16 warps of a CTA split K:
+// a warp takes a 128-segment of one or two blocks of up to 16 rows at a time, as fragments of mma.sync. A fragment's K order is free as long as x has the same: a lane's 16 bytes are 32 neighbouring K of one row.
 // The int4 group scale and the operand's factor (q4_operand.cuh) multiply the segment's sum in fp32.
 //
 // With few segments every CTA builds the operand itself in shared memory; with more, one kernel builds it once in the

@@ -2,9 +2,9 @@
 //
 // The weights are the M side of the MMA, decoded straight into tensor memory: a tile is up to 128 rows of W, and a
 // cluster of CTAs splits a tile's K, so that tiles of equal height and K ranges fill the SMs whatever N is (8192 rows: 74
-// tiles of 111 rows, two CTAs each). Two teams of four warps take 128-segments in turn (8192 x 8192 at T = 16: one team 23.5
-// us, four 24.0, two 21.6), a thread decoding one row's 128 codes to exact fp16; two warps issue the MMAs of a segment in turn (an instruction takes ~45 cycles to issue), each
-// into an accumulator of the segment's own; eight warps add the accumulators, times the rows' group scales and the
+// tiles of 111 rows, two CTAs each). Two teams of four warps take 128-segments in turn (8192 x 8192 at T = 16: one team
+// 23.5 us, two 21.6, four 24.0), a thread decoding one row's 128 codes to exact fp16; two warps issue the MMAs of a segment
+// in turn (an instruction takes ~45 cycles to issue), each into an accumulator of the segment's own; eight warps add the accumulators, times the rows' group scales and the
 // tokens' factors, to fp32 sums in registers: scales of any range and tokens of any magnitude lose nothing. At the end
 // the CTAs of a cluster exchange their sums through distributed shared memory and add them in rank order.
 // Codes come by TMA, 512 K of all rows per stage, the operand too, a pair of segments per stage, with its factors; rows
@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     if (lane == 0) {
       pdl_wait();
       const int tpad = (p.T + 3) & ~3, fbytes = min(TB, tpad - t0) * 4;
-      const float* fac = reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.workspace) + q4_rows_factors(p.T, all_segs)) + t0;
+      const uint8_t* img = static_cast<const uint8_t*>(p.workspace);
+      const float* fac = reinterpret_cast<const float*>(img + q4_rows_factors(p.T, all_segs)) + t0;
       int it = 0;
       for (; it < pairs; ++it) {
         const int slot = it % kMmPairStages, seg = 2 * it, n = min(2, segs - seg);
@@ -188,7 +189,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
         for (int j = 0; j < n; ++j)
           bulk_g2s(s_factor[(seg + j) % kMmRing], fac + static_cast<size_t>(seg0 + seg + j) * tpad, fbytes, &bb.b_full[slot]);
       }
-      for (int j = max(it - kMmPairStages, 0); j < it; ++j) mbar_wait_bounded(&bb.b_full[j % kMmPairStages], (j / kMmPairStages) & 1, 1000000);
+      for (int j = max(it - kMmPairStages, 0); j < it; ++j)
+        mbar_wait_bounded(&bb.b_full[j % kMmPairStages], (j / kMmPairStages) & 1, 1000000);
     }
   } else if (warp < 4) {
     // ---- MMA: segments of one parity. kMmA and kMmD are even, so that a place of either belongs to one warp; both
