@@ -72,7 +72,24 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
     const float2 a = pair_to_f32<TYPE>(raw[j].x), b = pair_to_f32<TYPE>(raw[j].y);
     v[j][0] = a.x, v[j][1] = a.y, v[j][2] = b.x, v[j][3] = b.y;
   }
-  if (rotate) {                                  // the butterfly of fwht128_warp, one fused multiply-add per step
+  float back[NP];                                // power of two taken out before the rotation
+#pragma unroll
+  for (int j = 0; j < NP; ++j) back[j] = 1.f;
+  if (rotate) {
+    // A sum of 128 bf16 values may pass fp32's range: a segment with values of 2^120 or more is rotated at 2^-8 of its size
+    // (exact but for values 2^-238 times the largest). fp16 values are far below.
+    if constexpr (TYPE == kTBf16) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float most = fmaxf(fmaxf(fabsf(v[j][0]), fabsf(v[j][1])), fmaxf(fabsf(v[j][2]), fabsf(v[j][3])));
+        if (__any_sync(0xFFFFFFFFu, most >= 0x1p120f)) {
+          back[j] = 0x1p8f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] *= 0x1p-8f;
+        }
+      }
+    }
+    // the butterfly of fwht128_warp, one fused multiply-add per step
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const float a = v[j][0] + v[j][1], b = v[j][0] - v[j][1], c = v[j][2] + v[j][3], d = v[j][2] - v[j][3];
@@ -109,7 +126,7 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
   for (int j = 0; j < NP; ++j) {
     const int e = min(max(static_cast<int>(m[j] >> 23), 15), 254);             // biased exponent of the largest value
     const float f = m[j] ? __uint_as_float(static_cast<uint32_t>(268 - e) << 23) : 1.f;          // 2^(141 - e)
-    float inv = m[j] ? __uint_as_float(static_cast<uint32_t>(e - 14) << 23) : 1.f;
+    float inv = m[j] ? back[j] * __uint_as_float(static_cast<uint32_t>(e - 14) << 23) : 1.f;
     uint2 u;
     int off;
     if constexpr (AR == kLimbs) {

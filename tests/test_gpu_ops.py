@@ -214,6 +214,34 @@ def test_q4_takes_the_quantisers_output():
         assert np.linalg.norm(y - want) <= 0.15 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("T", [1, 3, 8, 12, 33])
+def test_q4_rotation_near_the_top_of_bf16(T):
+    # x' = Hn x is a sum of 128 activations over sqrt(128): the sum passes fp32's range before x' does, and x' (of a segment
+    # of one sign) before the product with small scales does. Ordinary tokens and infinities stand beside such ones.
+    x, codes, scales, _ = q4_case("int4", 200, 384, T, torch.bfloat16, 40 + T, hot=False)
+    big = [0.0, 1e37, 3.3e38, 3.2e36][:T]
+    x = x.clone()
+    for t, v in enumerate(big):
+        if v:
+            x[t] = x[t].sign() * v
+            x[t, 128:256] = v if t % 2 else -v
+            x[t, 300] = 1e-30
+    if T > 5:
+        x[5, 7] = float("inf")
+        x[6] = -3.3e38
+    scales = (scales.float() * 2.0 ** -12).to(torch.bfloat16)
+    y = ops.q4_linear(x, codes, scales, None, fmt="int4", rotated=True)
+    keep = [t for t in range(T) if t != 5]
+    ref, slack = q4_reference(x[keep], codes, scales, None, "int4", True)
+    close(y[keep], ref, torch.bfloat16, slack, 2.0 ** -11)
+    if T > 5:
+        assert not torch.isfinite(y[5]).any()
+    # a power of two taken out of the whole input comes out of the whole output, bit for bit
+    small = ops.q4_linear((x.float() * 2.0 ** -40).to(torch.bfloat16), codes, (scales.float() * 2.0 ** 40).to(torch.bfloat16), None,
+                          fmt="int4", rotated=True)
+    assert torch.equal(small[keep], y[keep])
+
+
 # ------------------------------------------------------------------------------------------ grouped linear
 
 def counts_to_offsets(counts):
