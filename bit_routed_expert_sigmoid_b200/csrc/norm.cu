@@ -22,6 +22,21 @@ __device__ __forceinline__ float block_sum(float v, float* wsum) {
   return tot;
 }
 
+// 1 / sqrt(mean + eps) over the row, from the thread's sum of squares. Values from 2^56 on may have a sum that passes
+// fp32's range: all threads of the CTA then see it infinite and add the squares of 2^-80 times the values (`scaled`), at
+// most 32768 of 2^96, beside which eps is nothing. An infinite or NaN value stays what it is.
+template <bool WIDE, typename Scaled>
+__device__ __forceinline__ float inv_rms(float s, int H, float eps, float* wsum, Scaled scaled) {
+  const float sum = block_sum(s, wsum);
+  if constexpr (WIDE) {
+    if (sum > 3.402823466e38f) {
+      __syncthreads();                           // wsum is written again
+      return 0x1p-80f / sqrtf(block_sum(scaled(), wsum) / static_cast<float>(H));
+    }
+  }
+  return 1.0f / sqrtf(sum / static_cast<float>(H) + eps);
+}
+
 // Element k (of 8 VPT) of a thread: 8 neighbours per step with 16-byte accesses, else one element per step so
 // that a warp's accesses are neighbours.
 template <bool VEC>
@@ -143,7 +158,15 @@ __global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 8; ++j) s = fmaf(b[j], b[j], s);
     }
-    norm = 1.0f / sqrtf(block_sum(s, sum_post) / static_cast<float>(H) + p.eps);
+    norm = inv_rms<TYPE == kTBf16>(s, H, p.eps, sum_post, [&] {   // from memory: the widened row is not kept for this
+      float w = 0.f;
+#pragma unroll 1
+      for (int c = threadIdx.x; c < H; c += blockDim.x) {
+        const float b = 0x1p-80f * to_f32<TYPE>(p.y[t * p.ldy + c]);
+        w = fmaf(b, b, w);
+      }
+      return w;
+    });
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -203,12 +226,16 @@ __global__ void __launch_bounds__(kMaxThreads<VPT>) block_norm_kernel(const __gr
     }
   }
   if (!p.z) return;
-  float s = 0.f;
+  auto squares = [&](float k) {
+    float s = 0.f;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
+    for (int v = 0; v < VPT; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(x[v][j], x[v][j], s);   // columns behind H hold zeros
-  const float inv = 1.0f / sqrtf(block_sum(s, sum_pre) / static_cast<float>(H) + p.eps);
+      for (int j = 0; j < 8; ++j) s = fmaf(k * x[v][j], k * x[v][j], s);       // columns behind H hold zeros
+    return s;
+  };
+  // wide for any type: the scales of residual and branch may be large
+  const float inv = inv_rms<true>(squares(1.f), H, p.eps, sum_pre, [&] { return squares(0x1p-80f); });
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
 #pragma unroll

@@ -493,6 +493,41 @@ def test_block_norm_rows_are_independent_and_padding_is_kept():
     assert torch.all(z[0, :100] == 1) and torch.isnan(z[1, :100]).all() and torch.all(z[2, :100] == 0) and torch.all(z[:, 100:] == 5)
 
 
+@pytest.mark.parametrize("H", [40, 2048, 4100, 8200, 32768])
+@pytest.mark.parametrize("T", [3, 1030])
+def test_block_norm_of_values_whose_squares_pass_fp32(T, H):
+    # rows of ordinary size, of 1e25 and of nearly the largest bf16 value: the mean square does not fit fp32, the norm does
+    g = torch.Generator().manual_seed(H + T)
+    if T * H > 1 << 23:
+        T = 7
+    mag = torch.tensor([1.0, 1e25, 1e38])[torch.arange(T) % 3][:, None]
+    y = ((0.5 + torch.rand((T, H), generator=g)) * mag).to(torch.bfloat16).cuda()
+    x = (torch.randn((T, H), generator=g) * mag * 0.5).cuda()
+    pw = (1 + 0.1 * torch.randn(H, generator=g)).cuda()
+    fits = x.clamp(-1.5e38, 1.5e38)                  # some of x's largest values are infinite: those rows are looked at by themselves
+    for res in (x, x.to(torch.bfloat16), fits, fits.to(torch.bfloat16)):
+        rows = torch.isfinite(res).all(1).cpu().numpy()
+        assert rows[1] and (res is x or res.dtype != torch.float32 or rows.all())
+        for kw in (dict(post_norm=True, post_weight=pw), dict(branch_scale=0.5)):
+            xo, z = ops.block_norm(res, y, pre_weight=pw, **kw)
+            assert torch.all((z == 0) | torch.isnan(z) | torch.from_numpy(rows).cuda()[:, None])
+            xo, z, rs = xo[rows], z[rows], f64(res)[rows]
+            rx, rz = O.block_norm(rs, f64(y)[rows], pre_weight=f64(pw), **{k: f64(v) if k == "post_weight" else v for k, v in kw.items()})
+            sx = (np.abs(rs) + np.abs(rx - rs)) * 64 * 2.0 ** -24
+            if res.dtype == torch.float32:
+                assert np.all(np.abs(f64(xo) - rx) <= sx)
+            else:
+                close(xo, rx, torch.bfloat16, sx, 2.0 ** -14)
+            rms = np.sqrt((rx * rx).mean(1, keepdims=True) + 1e-6)
+            sz = (sx + np.abs(rx) * 64 * 2.0 ** -24) / rms * np.abs(f64(pw)) + np.abs(rz) * (
+                np.linalg.norm(sx, axis=1, keepdims=True) / np.linalg.norm(rx, axis=1, keepdims=True))
+            close(z, rz, torch.bfloat16, sz, 2.0 ** -14)
+    # infinities and NaN are no such rows: they go through as before
+    y[0, 0], y[1, 1] = float("inf"), float("nan")
+    _, z = ops.block_norm(torch.zeros_like(x), y)
+    assert torch.isnan(z[0, 0]) and torch.all(z[0, 1:] == 0) and torch.isnan(z[1]).all() and torch.isfinite(z[2]).all()
+
+
 # ------------------------------------------------------------------------------------------- used together
 
 def block_inputs(T, H=256, I=128, E=16, k=4, seed=0):
