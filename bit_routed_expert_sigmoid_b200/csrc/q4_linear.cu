@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) q4_ring_kernel(const __grid_c
       for (int j = 0; j < 4; ++j) {
         const int i = min(i0 + j * kQ4Warps, pairs - 1), t = i / segs, seg = i - t * segs;
         raw[j] = q4_fetch(p, t, seg);
-        o[j] = q4_place<kTokens>(sm_x, t, seg, p.T, segs);
+        o[j] = q4_place<kTokens, 1>(sm_x, t, seg, p.T, segs);
         if (i0 + j * kQ4Warps >= pairs) o[j].at = nullptr;
       }
       q4_operand<AR, TYPE, 4>(raw, p.rotated != 0, o);

@@ -4,11 +4,12 @@
 // cluster of CTAs splits a tile's K, so that tiles of equal height and K ranges fill the SMs whatever N is (8192 rows: 74
 // tiles of 111 rows, two CTAs each). Two teams of four warps take 128-segments in turn (8192 x 8192 at T = 16: one team
 // 23.5 us, two 21.6, four 24.0), a thread decoding one row's 128 codes to exact fp16; two warps issue the MMAs of a segment
-// in turn (an instruction takes ~45 cycles to issue), each into an accumulator of the segment's own; eight warps add the accumulators, times the rows' group scales and the
-// tokens' factors, to fp32 sums in registers: scales of any range and tokens of any magnitude lose nothing. At the end
-// the CTAs of a cluster exchange their sums through distributed shared memory and add them in rank order.
-// Codes come by TMA, 512 K of all rows per stage, the operand too, a pair of segments per stage, with its factors; rows
-// of codes that are no multiple of 16 bytes (K % 32 = 16) are read by the decoding warps themselves.
+// in turn (an instruction takes ~45 cycles to issue), each into an accumulator of the segment's own; eight warps add the
+// accumulators, times the rows' group scales and the tokens' factors, to fp32 sums in registers: scales of any range and
+// tokens of any magnitude lose nothing. At the end the CTAs of a cluster exchange their sums through distributed shared
+// memory and add them in rank order.
+// Codes come by TMA, 512 K of all rows per stage, the operand too, a pair of segments per stage (kF16Pair: the two parts of
+// one), with its factors; rows of codes that are no multiple of 16 bytes (K % 32 = 16) are read by the decoding warps.
 // 8192 x 8192 takes 20.1 us at T = 16 and 24.4 at T = 64, 5001 x 4112 NVFP4 15.6 at T = 37 (HBM 5.4, 5.6, 1.9). What bounds it
 // is the chain of a segment, 0.4 us a team: codes to registers, decoding, the store to tensor memory, eight MMAs, the
 // sums. More stages, more teams or codes released before they are decoded only made the warps wait for one another.
@@ -46,7 +47,7 @@ constexpr int kMmScaleBytes = 32 * 1024;
 
 struct MmParams {
   CUtensorMap tm_codes;                          // boxed: [K / 256][N][128 bytes], else [N][K / 2 bytes]
-  CUtensorMap tm_x;                              // operand [segs * 2][T][64] fp16, boxes of 4 x TB x 64
+  CUtensorMap tm_x;                              // operand [segs * parts * 2][T][64] fp16, boxes of 4 x TB x 64
   CUtensorMap tm_scales;                         // [N][scale bytes per row], boxes of scale_row x R
   Q4Params q;
   int R;                                         // rows of a tile
@@ -90,7 +91,8 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
 template <int AR, int TYPE, bool TMA>
 __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_constant__ MmParams mp) {
   const Q4Params& p = mp.q;
-  constexpr bool kI4 = AR == kF16Int4;
+  constexpr bool kI4 = AR != kF16Nvfp4;
+  constexpr int kSegs = 2 / kParts<AR>;          // segments of a stage of the operand: four 64-K blocks in all
   extern __shared__ uint8_t smem_raw[];
   __shared__ MmBars bb;
   __shared__ __align__(16) float s_factor[kMmRing][kMmTokens];   // of the tokens, per segment
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
   const int all_segs = (p.K + 127) / 128;
   const int rank = blockIdx.x % mp.split, tile = blockIdx.x / mp.split;
   const int seg0 = rank * mp.range, segs = max(min(mp.range, all_segs - seg0), 0);     // this CTA's segments
-  const int pairs = (segs + 1) / 2, chunks = (segs + kMmChunk - 1) / kMmChunk;
+  const int pairs = (segs + kSegs - 1) / kSegs, chunks = (segs + kMmChunk - 1) / kMmChunk;
   const int R = mp.R, TB = mp.TB, row0 = tile * R, rows = min(R, p.N - row0);
   const int b_stage = TB * 512, c_stage = TMA ? mm_code_stage(R) : 0;
   const int t0 = blockIdx.y * TB, N16 = (TB + 15) & ~15;
@@ -174,18 +176,18 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
       if (mp.scale_row) mbar_wait_bounded(&bb.scales, 0, 1000000);
     }
   } else if (warp == 1) {
-    // ---- operand: a pair's four 64-K blocks (blocks behind K read as zeros), and the segments' factors
+    // ---- operand: a stage's four 64-K blocks (blocks behind K read as zeros), and the segments' factors
     if (lane == 0) {
       pdl_wait();
       const int tpad = (p.T + 3) & ~3, fbytes = min(TB, tpad - t0) * 4;
       const uint8_t* img = static_cast<const uint8_t*>(p.workspace);
-      const float* fac = reinterpret_cast<const float*>(img + q4_rows_factors(p.T, all_segs)) + t0;
+      const float* fac = reinterpret_cast<const float*>(img + q4_rows_factors(p.T, all_segs, kParts<AR>)) + t0;
       int it = 0;
       for (; it < pairs; ++it) {
-        const int slot = it % kMmPairStages, seg = 2 * it, n = min(2, segs - seg);
+        const int slot = it % kMmPairStages, seg = kSegs * it, n = min(kSegs, segs - seg);
         if (it >= kMmPairStages && !pf_wait(&bb.b_empty[slot], ((it / kMmPairStages) - 1) & 1, abort, err)) break;
         mbar_arrive_expect_tx(&bb.b_full[slot], b_stage + n * fbytes);
-        tma_3d(sm_b + slot * b_stage, &mp.tm_x, 0, t0, 2 * (seg0 + seg), &bb.b_full[slot]);
+        tma_3d(sm_b + slot * b_stage, &mp.tm_x, 0, t0, 4 / kSegs * (seg0 + seg), &bb.b_full[slot]);
         for (int j = 0; j < n; ++j)
           bulk_g2s(s_factor[(seg + j) % kMmRing], fac + static_cast<size_t>(seg0 + seg + j) * tpad, fbytes, &bb.b_full[slot]);
       }
@@ -194,20 +196,20 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     }
   } else if (warp < 4) {
     // ---- MMA: segments of one parity. kMmA and kMmD are even, so that a place of either belongs to one warp; both
-    // warps go through all pairs of the operand.
+    // warps go through all stages of the operand.
     const int w = warp - 2;
     const uint32_t idesc = idesc_m128(N16, false);
     for (int it = 0; it < pairs; ++it) {
-      const int seg = 2 * it + w, sb = it % kMmPairStages, sa = seg % kMmA, sd = seg % kMmD;
+      const int seg = kSegs == 2 ? 2 * it + w : it, sb = it % kMmPairStages, sa = seg % kMmA, sd = seg % kMmD;
       if (!pf_wait_all(&bb.b_full[sb], (it / kMmPairStages) & 1, abort, err)) break;
-      if (seg < segs) {
+      if (seg < segs && (seg & 1) == w) {
         if (seg >= kMmD && !pf_wait_all(&bb.d_empty[sd], ((seg / kMmD) - 1) & 1, abort, err)) break;
         if (!pf_wait_all(&bb.a_full[sa], (seg / kMmA) & 1, abort, err)) break;
         tc_fence_after();
-        const uint32_t b0 = smem_u32(sm_b + sb * b_stage) + w * TB * 256;
+        const uint32_t b0 = smem_u32(sm_b + sb * b_stage) + (kSegs == 2 ? w * TB * 256 : 0);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_ta_w(tmem + sd * 64, tmem_a + sa * 64 + ks * 8, sdesc_sw128(b0 + (ks >> 2) * TB * 128 + (ks & 3) * 32), idesc,
+        for (int ks = 0; ks < 8 * kParts<AR>; ++ks)
+          tc_mma_ta_w(tmem + sd * 64, tmem_a + sa * 64 + (ks & 7) * 8, sdesc_sw128(b0 + (ks >> 2) * TB * 128 + (ks & 3) * 32), idesc,
                       ks ? 1u : 0u);
         tc_commit_w(&bb.a_empty[sa]);
         tc_commit_w(&bb.d_full[sd]);
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
         for (int i = 0; i < 4; ++i) {            // 32 codes: 16 columns
           uint32_t v[16];
           const uint32_t s2 = i < 2 ? scale.x : scale.y;
-          decode_f16<AR>(code[i], i & 1 ? s2 >> 16 : s2 & 0xFFFFu, v);
+          decode_f16<kI4 ? kF16Int4 : kF16Nvfp4>(code[i], i & 1 ? s2 >> 16 : s2 & 0xFFFFu, v);
           if (i == 0) {
             if (seg >= kMmA && !(ok = pf_wait_all(&bb.a_empty[sa], ((seg / kMmA) - 1) & 1, abort, err))) break;
             tc_fence_after();
@@ -404,7 +406,7 @@ int clusters_of(int dev, int sms, int k) {
 
 template <int AR, int TYPE, bool TMA>
 cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
-  constexpr bool kI4 = AR == kF16Int4;
+  constexpr bool kI4 = AR != kF16Nvfp4;
   int dev, sms;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
@@ -454,8 +456,8 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
                         : encode_words(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R)))
     return cudaErrorInvalidValue;
   if (mp.scale_row && !encode_words_rows(&mp.tm_scales, p.scales, p.N, scale_row, mp.scale_row, mp.R)) return cudaErrorInvalidValue;
-  if (!encode_16bit_blocks(&mp.tm_x, p.workspace, false, p.T, static_cast<uint64_t>(segs) * 128, static_cast<uint64_t>(segs) * 128,
-                           mp.TB, 4))
+  const uint64_t cols = static_cast<uint64_t>(segs) * 128 * kParts<AR>;
+  if (!encode_16bit_blocks(&mp.tm_x, p.workspace, false, p.T, cols, cols, mp.TB, 4))
     return cudaErrorInvalidValue;
   if ((e = allow_smem_once<q4_mma_kernel<AR, TYPE, TMA>>(dev, kMost)) != cudaSuccess) return e;
   if ((e = launch_q4_operand<AR, TYPE, kRows>(p, sms, s)) != cudaSuccess) return e;
@@ -479,7 +481,10 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_q4_mma(const Q4Params& p, cudaStream_t s) {
-  if (p.fmt == kInt4) return p.type == kTBf16 ? launch_mm<kF16Int4, kTBf16, true>(p, s) : launch_mm<kF16Int4, kTF16, true>(p, s);
+  if (p.fmt == kInt4) {
+    if (p.type == kTBf16) return launch_mm<kF16Int4, kTBf16, true>(p, s);
+    return p.rotated ? launch_mm<kF16Pair, kTF16, true>(p, s) : launch_mm<kF16Int4, kTF16, true>(p, s);
+  }
   if (p.K % 32 == 0)
     return p.type == kTBf16 ? launch_mm<kF16Nvfp4, kTBf16, true>(p, s) : launch_mm<kF16Nvfp4, kTF16, true>(p, s);
   return p.type == kTBf16 ? launch_mm<kF16Nvfp4, kTBf16, false>(p, s) : launch_mm<kF16Nvfp4, kTF16, false>(p, s);

@@ -11,26 +11,37 @@ namespace {
 // How codes meet x, per 128-segment:
 //   kF16Int4, kF16Nvfp4  codes become exact fp16 (int4: -8..7; NVFP4: E2M1 x E4M3, six significant bits); x is fp16
 //              after one power of two per (token, segment) that brings the segment's largest finite value into [2^14,
-//              2^15): 16-bit inputs stay exact down to 2^-29 of it (2^-38 absolute), rotated ones are rounded to fp16's
-//              11 bits. The factor is taken out of the fp32 sum again, so no range is lost for either type.
+//              2^15): 16-bit inputs stay exact down to 2^-29 of it (2^-38 absolute). The factor is taken out of the fp32 sum
+//              again. Rotated bf16 inputs are rounded to fp16's 11 bits, an eighth of the output's rounding: 2.0e-4 of the
+//              result's norm beside 1.66e-3.
+//   kF16Pair   rotated int4 of fp16 inputs, more tokens: there the same rounding would be as large as the output's (2.9e-4 of
+//              the norm in all against 2.07e-4), so Hn x enters as the sum of two fp16 numbers, 22 bits, at twice the MMAs:
+//              8192 x 8192 takes 24.9 us at T = 16 and 30.2 at T = 64, where one number takes 20.3 and 24.6. Six stages of the
+//              operand instead of three: 26.5 and 33.6. An infinity's second part is NaN.
 //   kLimbs     rotated int4, few tokens: Hn x is rounded to 16-bit fixed point per (token, segment), a unit being 2^-14
 //              of the power of two below the segment's largest value (rotation spreads outliers, so that is finer than
 //              fp16 for all but the smallest values); its signed high and unsigned low bytes multiply the exact int8
 //              16 c on the integer tensor cores. Three instructions decode eight codes instead of nine.
-enum Arith : int { kF16Int4, kF16Nvfp4, kLimbs };
+enum Arith : int { kF16Int4, kF16Nvfp4, kLimbs, kF16Pair };
+
+// fp16 numbers per element of the operand
+template <int AR>
+constexpr int kParts = AR == kF16Pair ? 2 : 1;
 
 // A (token, segment) is four chunks of 16 bytes for each of the four lanes q that read it, K = 32 q .. 32 q + 31. fp16:
 // chunk i holds K = 32 q + 8 i .. + 7 in the order of the decoded pairs (int4 0,4,1,5,2,6,3,7; NVFP4 0,1,2,6,4,5,3,7);
 // limbs: chunk 2 limb + (i >> 1) holds at 8 (i & 1) the bytes of K = 32 q + 8 i + 0, 2, 4, 6 and of + 1, 3, 5, 7.
 //   kTokens  [segment][token][chunk][q], then the inverse factor, kTokenBytes each
-//   kRows    [token][segment][q][chunk]: K-major rows; then the factors [segment][tokens rounded up to 4]
+//   kRows    [token][segment][part][q][chunk]: K-major rows; then the factors [segment][tokens rounded up to 4]
 // kTokens is for up to 8 tokens (q4_linear.cu), kRows for more (q4_mma.cu).
 enum OperandLayout : int { kTokens, kRows };
 constexpr int kTokenBytes = 272;
 
-__host__ __device__ inline size_t q4_rows_factors(int T, int segs) { return static_cast<size_t>(T) * segs * 256; }
+__host__ __device__ inline size_t q4_rows_factors(int T, int segs, int parts) { return static_cast<size_t>(T) * segs * parts * 256; }
+// of the form that takes most (more than 8 tokens: two parts)
 __host__ __device__ inline size_t q4_operand_bytes(int T, int segs) {
-  return T <= 8 ? static_cast<size_t>(T) * segs * kTokenBytes : q4_rows_factors(T, segs) + static_cast<size_t>((T + 3) & ~3) * segs * 4;
+  return T <= 8 ? static_cast<size_t>(T) * segs * kTokenBytes
+                : q4_rows_factors(T, segs, 2) + static_cast<size_t>((T + 3) & ~3) * segs * 4;
 }
 
 struct OperandPlace {
@@ -39,7 +50,7 @@ struct OperandPlace {
   float* factor;
 };
 
-template <int LAYOUT>
+template <int LAYOUT, int PARTS>
 __device__ __forceinline__ OperandPlace q4_place(uint8_t* img, int t, int seg, int T, int segs) {
   OperandPlace o;
   if constexpr (LAYOUT == kTokens) {
@@ -47,9 +58,9 @@ __device__ __forceinline__ OperandPlace q4_place(uint8_t* img, int t, int seg, i
     o.chunk = 64, o.lane = 16;
     o.factor = reinterpret_cast<float*>(o.at + 256);
   } else {
-    o.at = img + (static_cast<size_t>(t) * segs + seg) * 256;
+    o.at = img + (static_cast<size_t>(t) * segs + seg) * (256 * PARTS);
     o.chunk = 16, o.lane = 64;
-    o.factor = reinterpret_cast<float*>(img + q4_rows_factors(T, segs)) + static_cast<size_t>(seg) * ((T + 3) & ~3) + t;
+    o.factor = reinterpret_cast<float*>(img + q4_rows_factors(T, segs, PARTS)) + static_cast<size_t>(seg) * ((T + 3) & ~3) + t;
   }
   return o;
 }
@@ -127,7 +138,7 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
     const int e = min(max(static_cast<int>(m[j] >> 23), 15), 254);             // biased exponent of the largest value
     const float f = m[j] ? __uint_as_float(static_cast<uint32_t>(268 - e) << 23) : 1.f;          // 2^(141 - e)
     float inv = m[j] ? back[j] * __uint_as_float(static_cast<uint32_t>(e - 14) << 23) : 1.f;
-    uint2 u;
+    uint2 u, low = make_uint2(0, 0);             // low: kF16Pair's second part
     int off;
     if constexpr (AR == kLimbs) {
       uint32_t n[4];
@@ -146,11 +157,18 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] *= f;
-      if constexpr (AR == kF16Int4) {
-        const float r0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j][0] : v[j][2], 1);
-        const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j][1] : v[j][3], 1);
-        u = odd ? make_uint2(pack_half2(r0, v[j][2]), pack_half2(r1, v[j][3]))
-                : make_uint2(pack_half2(v[j][0], r0), pack_half2(v[j][1], r1));
+      if constexpr (AR == kF16Int4 || AR == kF16Pair) {
+        auto pairs = [&](const float (&w)[4]) {
+          const float r0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[0] : w[2], 1);
+          const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[1] : w[3], 1);
+          return odd ? make_uint2(pack_half2(r0, w[2]), pack_half2(r1, w[3])) : make_uint2(pack_half2(w[0], r0), pack_half2(w[1], r1));
+        };
+        u = pairs(v[j]);
+        if constexpr (AR == kF16Pair) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] -= __half2float(__float2half_rn(v[j][i]));       // exact
+          low = pairs(v[j]);
+        }
       } else {                                   // 0,1,2,6 by the even lane of a pair, 4,5,3,7 by the odd one
         const float r = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j][2] : v[j][3], 1);
         u = odd ? make_uint2(pack_half2(v[j][0], v[j][1]), pack_half2(r, v[j][3]))
@@ -161,6 +179,7 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
     }
     if (o[j].at) {
       *reinterpret_cast<uint2*>(o[j].at + (lane >> 3) * o[j].lane + off) = u;
+      if constexpr (AR == kF16Pair) *reinterpret_cast<uint2*>(o[j].at + 256 + (lane >> 3) * o[j].lane + off) = low;
       if (lane == 0) *o[j].factor = inv;
     }
   }
@@ -178,7 +197,7 @@ __global__ void __launch_bounds__(256) q4_operand_kernel(const __grid_constant__
        i += static_cast<long long>(gridDim.x) * 8) {
     const int t = static_cast<int>(i / segs), seg = static_cast<int>(i - static_cast<long long>(t) * segs);
     const uint2 raw[1] = {q4_fetch(p, t, seg)};
-    const OperandPlace o[1] = {q4_place<LAYOUT>(static_cast<uint8_t*>(p.workspace), t, seg, p.T, segs)};
+    const OperandPlace o[1] = {q4_place<LAYOUT, kParts<AR>>(static_cast<uint8_t*>(p.workspace), t, seg, p.T, segs)};
     q4_operand<AR, TYPE, 1>(raw, p.rotated != 0, o);
   }
 }

@@ -36,8 +36,8 @@ extern "C" {
  * 8; y, ldy need no alignment beyond their element's. K, T <= 65536, N <= 2^30, N * K <= 2^37. Made for few tokens
  * (T <= 64): larger T run in chunks that read the weights again. T = 0 is a no-op.
  * Rounding before the sums: rotated activations, per (token, 128-segment), to 16-bit fixed point of the segment's
- * largest value (T <= 8) or, scaled by a power of two, to fp16 (T > 8). Unrotated ones, and the codes times NVFP4's
- * block scales, enter exactly, but for activations below 2^-29 of their segment's largest.
+ * largest value (T <= 8) or, scaled by a power of two, to fp16's 11 bits (T > 8, BF16) or 22 bits (T > 8, F16). Unrotated
+ * ones, and the codes times NVFP4's block scales, enter exactly, but for activations below 2^-29 of their segment's largest.
  * workspace: flint_q4_linear_workspace_size(K, T) bytes of device memory (the activations as the kernel's operand),
  * 256-byte aligned, in use until the call's work is done; may be NULL when that size is 0, as it is for the smallest
  * calls. The size is 0 for invalid arguments too. */

@@ -242,6 +242,22 @@ def test_q4_rotation_near_the_top_of_bf16(T):
     assert torch.equal(small[keep], y[keep])
 
 
+@pytest.mark.parametrize("N,K,T", [(515, 2048, 9), (515, 2048, 24), (1000, 1152, 37), (300, 4096, 64), (260, 640, 129), (4096, 128, 70)])
+def test_q4_rotated_fp16_keeps_the_outputs_rounding(N, K, T):
+    # y = round(v), v off the exact value by e: the rounding and e are independent, so |y - ref|^2 is |round(ref) - ref|^2 +
+    # |e|^2 up to its scatter. x' = hi + lo, two fp16 numbers, leaves |e| below 2^-20 of the norm; x' as one fp16 number is
+    # 2^-12.3 off and breaks the bound of 2^-13. The scatter: squares of n roundings, each in [0, (1/2 step)^2], add up to
+    # their mean within 4 / sqrt(n) of it.
+    x, codes, scales, _ = q4_case("int4", N, K, T, torch.float16, N + K + T, hot=False)
+    scales = (scales.float() * 64).to(torch.bfloat16)            # outputs far above fp16's smallest normal
+    y = f64(ops.q4_linear(x, codes, scales, None, fmt="int4", rotated=True))
+    ref, _ = q4_reference(x, codes, scales, None, "int4", True)
+    r = ref.astype(np.float16).astype(np.float64)
+    assert np.isfinite(r).all()
+    got, least = np.sum((y - ref) ** 2), np.sum((r - ref) ** 2)
+    assert got <= (1 + 4 / np.sqrt(ref.size)) * least + (2.0 ** -13 * np.linalg.norm(ref)) ** 2, (got, least)
+
+
 # ------------------------------------------------------------------------------------------ grouped linear
 
 def counts_to_offsets(counts):
