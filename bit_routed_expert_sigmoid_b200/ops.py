@@ -2,8 +2,9 @@
 
 As in `layer`, PyTorch supplies device memory and streams only; every step runs in the library's CUDA
 kernels. Shapes, types and strides are checked here (ValueError) or by the C entry points (FlintError).
-Outputs that are not given are allocated; no gradients are recorded. Work goes to `stream` (default: the current stream of the
-inputs' device); an input written on another stream must have been ordered before it by the caller.
+Outputs that are not given are allocated; no gradients are recorded. Work goes to `stream` (default: the current stream of
+the inputs' device); an input written on another stream must have been ordered before it by the caller. With `stream`, the
+call's tensors are recorded on it, so that they may be dropped as soon as the call returns, and allocated outputs belong to it.
 
 The smallest calls take a few microseconds on the device, so the common path (tensors of the current
 device, its current stream) goes straight to the entry point.
@@ -37,6 +38,13 @@ def _elsewhere(device, stream) -> bool:
     return stream is not None or device.type != "cuda" or device.index != _current_device()
 
 
+def _used_on(stream, *values) -> None:
+    """The memory of the tensors among `values` is not handed out again before the work that `stream` then holds is done."""
+    for v in values:
+        if isinstance(v, torch.Tensor) and v.device.type == "cuda":
+            v.record_stream(stream)
+
+
 def _switched(fn, device, stream, *args, **kw):
     """fn with `stream` current (its device too), or with the tensors' device current."""
     if device.type != "cuda":
@@ -45,8 +53,11 @@ def _switched(fn, device, stream, *args, **kw):
         with torch.cuda.device(device):
             return fn(*args, **kw)
     _need(stream.device == device, "the stream belongs to another device than the tensors")
-    with torch.cuda.stream(stream):
-        return fn(*args, **kw)
+    try:
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    finally:
+        _used_on(stream, *args, *kw.values())
 
 
 def _need(ok: bool, what: str) -> None:
@@ -290,6 +301,8 @@ class FlintExperts16:
         """y[t] = scale * sum_k w[t][k] E_ids[t][k](x[t]) + addend[t]: ids int32 [T][top_k] (outside [0, E):
         no expert), w f32 [T][top_k], addend [T][H] (a shared expert's output)."""
         if _elsewhere(x.device, stream):
+            if stream is not None:
+                _used_on(stream, self.gate_up, self.down)
             return _switched(self.forward, x.device, stream, x, ids, w, addend=addend, scale=scale)
         _need(x.dim() == 2 and ids.dim() == 2 and x.shape[0] == ids.shape[0], "x [T][H] and ids [T][top_k]")
         offsets, perm, inv = expert_permute(ids, self.E)

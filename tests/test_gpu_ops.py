@@ -629,6 +629,61 @@ def test_two_streams_at_once():
                 assert torch.equal(u, v)
 
 
+def test_inputs_may_be_dropped_while_another_stream_still_reads_them():
+    # the stream is busy when each call returns; what the caller then drops, and writes to next, must not reach the call
+    s = torch.cuda.Stream()
+
+    def fresh(i):
+        d = block_inputs(24, seed=30 + i)
+        return d, ops.FlintExperts16(d["gu"], d["dn"])
+
+    def steps(d, ex, stream):
+        q = ops.q4_linear(d["y"], *d["q"], fmt="int4", stream=stream)
+        off, perm, inv = ops.expert_permute(d["ids"], 16, stream=stream)
+        h = ops.grouped_linear(d["y"], d["gu"], off, rows=perm, row_div=4, act="swiglu", stream=stream)
+        y = ex.forward(d["y"], d["ids"], d["w"], addend=q, stream=stream)
+        c = ops.expert_combine(h, inv, d["w"], stream=stream)
+        return q, off, perm, inv, h, y, c, *ops.block_norm(d["x"], d["y"], stream=stream)
+
+    for i in range(2):
+        d, ex = fresh(i)
+        live = int(steps(d, ex, None)[1][-1])
+        want = [t.clone() for t in steps(d, ex, None)]
+        s.wait_stream(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)           # about 50 ms
+        got = steps(d, ex, s)
+        shapes = [(t.shape, t.dtype) for k, v in d.items() for t in (v if isinstance(v, tuple) else (v,)) if t is not None]
+        del d, ex
+        over = [torch.full(shape, 77, dtype=dtype, device="cuda") for shape, dtype in shapes for _ in range(2)]
+        assert not s.query()                         # the calls had not even begun
+        torch.cuda.synchronize()
+        for j, (a, b) in enumerate(zip(got, want)):
+            if j == 4:                               # rows of no expert are not written
+                a, b = a[:live], b[:live]
+            assert torch.equal(a, b)
+        del over
+
+
+def test_a_stream_argument_inside_a_capture():
+    d = block_inputs(9, seed=8)
+    ex = ops.FlintExperts16(d["gu"], d["dn"])
+    want = [t.clone() for t in block_step(d, ex)]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        out = block_step(d, ex, stream=side)
+        here.wait_stream(side)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
 def test_no_rows_are_no_ops():
     e = torch.empty
     bf = torch.bfloat16

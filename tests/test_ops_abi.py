@@ -1,7 +1,9 @@
 """Argument checks of the standalone operators on the host, before any launch. No GPU needed: the pointers
 are never dereferenced."""
 
+import contextlib
 import ctypes
+import types
 
 import pytest
 import torch
@@ -155,3 +157,35 @@ def test_wrappers_refuse_other_scale_types(monkeypatch):
                         ("int4", torch.zeros((4, 2), dtype=torch.bfloat16))):
         with pytest.raises(ValueError, match="scales"):
             ops.q4_linear(x, codes, scales, torch.ones(1), fmt=fmt, rotated=False)
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that passes for one of device 0 and notes the streams it is recorded on."""
+
+    device = property(lambda self: torch.device("cuda", 0))
+
+    def record_stream(self, stream):
+        self.streams = getattr(self, "streams", []) + [stream]
+
+
+def test_tensors_of_a_call_on_another_stream_are_recorded_there(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(ops, "_current_device", lambda: 0)
+    stream = types.SimpleNamespace(device=torch.device("cuda", 0))
+    a, b, c, d = (torch.zeros(1).as_subclass(_OnDevice) for _ in range(4))
+    assert ops._switched(lambda x, k, z=None, f=0: x, a.device, stream, a, 3, z=b, f=1.5) is a
+    assert a.streams == b.streams == [stream]
+
+    def fails(x, y):
+        raise ValueError("refused behind a launch")
+    with pytest.raises(ValueError, match="refused"):
+        ops._switched(fails, a.device, stream, c, torch.zeros(1))
+    assert c.streams == [stream]
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    ops._switched(lambda x: x, a.device, None, d)
+    assert not hasattr(d, "streams")
+    # the experts' weights as well, which are no arguments of the call
+    ex = ops.FlintExperts16(torch.zeros((2, 4, 8)).as_subclass(_OnDevice), torch.zeros((2, 8, 2)).as_subclass(_OnDevice))
+    with pytest.raises(ValueError):
+        ex.forward(a, b, c, stream=stream)
+    assert ex.gate_up.streams == ex.down.streams == [stream]
