@@ -2,6 +2,9 @@
 
 PyTorch only allocates device memory and provides streams here; every step of the forward runs in
 the library's CUDA kernels (binding.flint_moe_forward).
+
+A call with `stream` records its tensors on that stream (and the layer its own memory), so that they may be dropped as soon
+as it returns; an allocated output belongs to `stream`. Inputs written on another stream are ordered before it by the caller.
 """
 
 from __future__ import annotations
@@ -21,6 +24,13 @@ def _to_device(a, device):
     if a.dtype == np.uint16:
         a = a.view(np.int16)
     return torch.from_numpy(a).to(device)
+
+
+def _record(stream, *tensors):
+    """Their memory is not handed out again before the work that `stream` then holds is done."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 # W4A4 intermediates (permuted rows): columns per row (0: one value per row) and dtype
@@ -70,6 +80,7 @@ class FlintMoELayer:
         self.ws_ptr = (base + 255) // 256 * 256
         self.handle = B.flint_moe_create(self.cfg, self.weights, self.ws_ptr, self.ws_bytes)
         self.cache = None
+        self._recorded = set()                   # streams that the layer's own memory is recorded on
         if n_slots > 0:
             hp = {k: (v.data_ptr() if v is not None else None) for k, v in self.host.items()}
             self.host_weights = B.flint_moe_weights(**hp)
@@ -78,11 +89,25 @@ class FlintMoELayer:
     def weight_bytes(self) -> int:
         return sum(v.numel() * v.element_size() for v in self.tensors.values() if v is not None)
 
+    def _on_stream(self, stream, *tensors):
+        """Records the tensors and the layer's memory on the stream of a call that named one."""
+        if stream is None:
+            return
+        _record(stream, *tensors)
+        if stream not in self._recorded:
+            _record(stream, self.workspace, *self.tensors.values())
+            self._recorded.add(stream)
+
+    def _output(self, T: int, stream) -> torch.Tensor:
+        with torch.cuda.stream(stream):          # of the current stream when None
+            return torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: [T][H] bf16 (or int16 bit patterns) on the device. Returns y [T][H] bf16."""
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+            y = self._output(T, stream)
+        self._on_stream(stream, x, y)
         s = (stream or torch.cuda.current_stream(self.device)).cuda_stream
         if self.cache is not None:
             B.flint_moe_forward_cached(self.handle, self.cache, x.data_ptr(), T, y.data_ptr(), s)
@@ -95,7 +120,8 @@ class FlintMoELayer:
         """Forward on a given routing: ids int32 [T][top_k] (ascending per token), w f32 [T][top_k]."""
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+            y = self._output(T, stream)
+        self._on_stream(stream, x, ids, w, y)
         s = (stream or torch.cuda.current_stream(self.device)).cuda_stream
         B.flint_moe_forward_routed(self.handle, x.data_ptr(), T, ids.data_ptr(), w.data_ptr(), y.data_ptr(), s)
         return y
@@ -106,6 +132,7 @@ class FlintMoELayer:
 
     def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, stream=None) -> None:
         """x_host, y_host: [T][H] 16-bit host tensors (pinned for asynchronous copies)."""
+        self._on_stream(stream)
         s = (stream or torch.cuda.current_stream(self.device)).cuda_stream
         B.flint_moe_forward_host(self.handle, x_host.data_ptr(), x_host.shape[0], y_host.data_ptr(), s)
 
@@ -175,6 +202,10 @@ class FlintMoEStack:
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
         """x: [T][H] fp32 residual on the device, updated in place and returned."""
         T = x.shape[0]
+        if stream is not None:
+            _record(stream, x, self.z, self.y)
+            for layer in self.layers:
+                layer._on_stream(stream)
         s = (stream or torch.cuda.current_stream(self.device)).cuda_stream
         B.flint_moe_stack_forward([layer.handle for layer in self.layers], x.data_ptr(), T, self.eps,
                                   self.z.data_ptr(), self.y.data_ptr(), s)

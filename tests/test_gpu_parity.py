@@ -304,3 +304,30 @@ def test_prefill_nvfp4_skewed_loads():
     dev, xd, y, ref, st = full_check(L, x)
     counts = np.diff(ref["offsets"])
     assert counts.max() > 300 and (counts == 0).any()
+
+
+@pytest.mark.parametrize("T", [8, 40])
+def test_tensors_and_layer_may_be_dropped_while_another_stream_works(T):
+    # the stream is busy when the call returns; what the caller then drops, and allocates and writes next, must not reach it
+    L = layer(32, "int4")
+    x = S.make_workload_x(T, 32)
+    want = y_to_host_bits(run(L, x)[2])
+    s = torch.cuda.Stream()
+    dev = FlintMoELayer(L, t_max=T)
+    dx = x_to_device(x)
+    shapes = [(t.shape, t.dtype) for t in (dx, dev.workspace, *dev.tensors.values()) if t is not None]
+    for _, dtype in shapes:                          # loads the kernels that fill memory below
+        torch.empty(1, dtype=dtype, device="cuda").fill_(1)
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)               # about 0.2 s
+    y = dev.forward(dx, stream=s)
+    keep = dev.handle                                # destroyed by close() below, behind the work
+    dev.tensors, dev.workspace, dx = {}, None, None
+    over = [torch.empty(shape, dtype=dtype, device="cuda").fill_(77) for shape, dtype in shapes]
+    assert keep and not s.query()                    # the call had not even begun
+    torch.cuda.synchronize()
+    assert np.array_equal(y_to_host_bits(y), want)
+    del over
+    dev.close()
