@@ -65,6 +65,15 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+# Sizes cross the C boundary as 32-bit integers, which ctypes would cut without a word. Checked all at once: their OR has a
+# high bit, or the sign, where one of them has it.
+_INT_MAX = 2 ** 31 - 1
+
+
+def _refuse_size() -> None:
+    raise ValueError("a negative size, or one of 2^31 or more: the operators take at most 2^31 - 1")
+
+
 def _together(device, *tensors) -> None:
     for t in tensors:
         if t is not None and t.device != device:
@@ -95,6 +104,8 @@ def q4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tscale
     ldx = _rows(x, "x")
     T, K = x.shape
     N = codes.shape[0]
+    if not 0 <= (T | K | N) <= _INT_MAX:
+        _refuse_size()
     group = 128 if fmt == "int4" else 16
     if codes.dtype != torch.uint8 or codes.shape != (N, K // 2) or K % 2 or not codes.is_contiguous():
         raise ValueError("codes must be contiguous u8 [N][K/2]")
@@ -124,6 +135,8 @@ def quantize_linear(w: torch.Tensor, *, fmt: str = "int4", rotate: bool = True, 
     _need(fmt in _FORMATS and w.dtype == torch.bfloat16 and w.dim() == 2 and w.is_contiguous(),
           "w must be contiguous bf16 [N][K]")
     N, K = w.shape
+    if not 0 <= (N | K) <= _INT_MAX:
+        _refuse_size()
     _need(N > 0 and K % (128 if fmt == "int4" else 16) == 0, "K must be a multiple of the scale group")
     s = _stream_of(w.device.index)
     codes = w.new_empty((N, K // 2), dtype=torch.uint8)
@@ -162,6 +175,8 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, r
         if rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous():
             raise ValueError("rows must be contiguous int32 [P]")
         P = rows.shape[0]
+    if not 0 <= (E | N | K | x.shape[0] | P | row_div) <= _INT_MAX:
+        _refuse_size()
     _together(dev, w, offsets, rows, y)
     nout = N // 2 if a else N
     if y is None:
@@ -184,6 +199,8 @@ def expert_permute(ids: torch.Tensor, n_experts: int, *, stream=None) -> tuple:
     if ids.dtype != torch.int32 or ids.dim() != 2 or not ids.is_contiguous() or n_experts < 1:
         raise ValueError("ids must be contiguous int32 [T][top_k], and at least one expert")
     T, K = ids.shape
+    if not 0 <= (T | K | n_experts) <= _INT_MAX:
+        _refuse_size()
     offsets, perm, inv = ids.new_empty((n_experts + 1,)), ids.new_empty((T * K,)), ids.new_empty((T, K))
     B.flint_expert_permute(ids.data_ptr(), T, K, n_experts, offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(),
                            _stream_of(dev.index))
@@ -207,6 +224,8 @@ def expert_combine(o: torch.Tensor, inv: torch.Tensor, w: torch.Tensor, *, adden
         raise ValueError("w must be contiguous f32 [T][top_k]")
     T, K = inv.shape
     P, H = o.shape
+    if not 0 <= (T | K | P | H) <= _INT_MAX:
+        _refuse_size()
     add = lda = 0
     if addend is not None:
         _need(addend.shape == (T, H) and addend.dtype == o.dtype, "addend must be [T][H] of o's type")
@@ -240,6 +259,8 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: boo
     ldx = _rows(x, "x")
     shape = x.shape
     T, H = shape
+    if not 0 <= (T | H) <= _INT_MAX:
+        _refuse_size()
     xt = x.dtype
     dt = y.dtype if y is not None else z.dtype if z is not None else z_dtype or (
         xt if xt in _TYPES else torch.bfloat16)

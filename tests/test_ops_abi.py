@@ -189,3 +189,30 @@ def test_tensors_of_a_call_on_another_stream_are_recorded_there(monkeypatch):
     with pytest.raises(ValueError):
         ex.forward(a, b, c, stream=stream)
     assert ex.gate_up.streams == ex.down.streams == [stream]
+
+
+def test_wrappers_refuse_sizes_that_pass_32_bits(monkeypatch):
+    # meta tensors stand for the large ones; nothing must reach the library, which would see the sizes modulo 2^32
+    monkeypatch.setattr(ops, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(ops, "_stream_of", lambda index: 0)
+    for name in ("flint_q4_linear", "flint_grouped_linear", "flint_expert_permute", "flint_expert_combine", "flint_block_norm"):
+        monkeypatch.setattr(ops.B, name, lambda *a, name=name: pytest.fail(f"{name} was called"))
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+
+    def m(*shape, dtype=bf):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    big = (1 << 32) + 5
+    for call in (lambda: ops.q4_linear(m(big, 128), m(4, 64, dtype=u8), m(4, 1)),
+                 lambda: ops.q4_linear(m(2, 128), m(big, 64, dtype=u8), m(big, 1)),
+                 lambda: ops.grouped_linear(m(big, 8), m(2, 4, 8), m(3, dtype=i32)),
+                 lambda: ops.grouped_linear(m(big, 8), m(2, 4, 8), m(3, dtype=i32), rows=m(9, dtype=i32)),
+                 lambda: ops.grouped_linear(m(9, 8), m(2, 4, 8), m(3, dtype=i32), rows=m(9, dtype=i32), row_div=big),
+                 lambda: ops.grouped_linear(m(9, 8), m(2, 4, 8), m(3, dtype=i32), rows=m(9, dtype=i32), row_div=5 - (1 << 32)),
+                 lambda: ops.expert_permute(m(big, 1, dtype=i32), 4),
+                 lambda: ops.expert_permute(m(3, 1, dtype=i32), big),
+                 lambda: ops.expert_combine(m(4, 8), m(big, 1, dtype=i32), m(big, 1, dtype=torch.float32)),
+                 lambda: ops.expert_combine(m(big, 8), m(4, 1, dtype=i32), m(4, 1, dtype=torch.float32)),
+                 lambda: ops.block_norm(m(big, 1)), lambda: ops.block_norm(m(1, big))):
+        with pytest.raises(ValueError, match="at most 2"):
+            call()
