@@ -654,6 +654,7 @@ cudaError_t launch_grouped_linear(const GroupedParams& p, cudaStream_t s) {
 // Reads and clears the current device's word (waits for the device's work).
 cudaError_t read_ops_error(unsigned* out) {
   const unsigned zero = 0;
+  *out = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(out, g_ops_error, sizeof(unsigned));
   if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_ops_error, &zero, sizeof(unsigned));

@@ -6,6 +6,8 @@ Outputs that are not given are allocated; no gradients are recorded. Work goes t
 the inputs' device); an input written on another stream must have been ordered before it by the caller. With `stream`, the
 call's tensors are recorded on it, so that they may be dropped as soon as the call returns, and allocated outputs belong to it.
 
+Waits inside the kernels are bounded. Should one give up, its call's output is incomplete and `error_word` says so.
+
 The smallest calls take a few microseconds on the device, so the common path (tensors of the current
 device, its current stream) goes straight to the entry point.
 """
@@ -303,6 +305,14 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: boo
     return x_out, z
 
 
+def error_word(device=None) -> int:
+    """0, or the timeout bit (4) when a wait inside a kernel of q4_linear or grouped_linear gave up on this device (default:
+    the current one) since the last call: what that kernel wrote is incomplete. Waits for the device and clears the word
+    (flint_ops_error_word)."""
+    with torch.cuda.device(device):
+        return B.flint_ops_error_word()
+
+
 class FlintExperts16:
     """The layer's routed experts kept in 16 bits (the type their checkpoint has them in, before
     flint_quantize_*), run on a routing the caller gives, as FlintMoELayer.forward_routed runs the 4-bit ones.
@@ -316,6 +326,10 @@ class FlintExperts16:
               "gate_up must be [E][2I][H] and down [E][H][I] of one type")
         self.gate_up, self.down = gate_up, down
         self.E, self.H, self.I = E, H, two_i // 2
+
+    def error_word(self) -> int:
+        """The operators' error word of the weights' device (ops.error_word)."""
+        return error_word(self.gate_up.device)
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, *, addend: torch.Tensor | None = None,
                 scale: float = 1.0, stream=None) -> torch.Tensor:

@@ -109,8 +109,8 @@ typedef struct flint_norm_args {
 flint_status flint_block_norm(const flint_norm_args* args, void* stream);
 
 /* Reads and clears the operators' error word of the current device: 0, or the timeout bit (4) when a bounded wait
- * inside a kernel of flint_q4_linear or flint_grouped_linear gave up since the last call (its output is then incomplete). Waits for
- * the device. */
+ * inside a kernel of flint_q4_linear or flint_grouped_linear gave up since the last call (its output is then
+ * incomplete). Waits for the device. */
 flint_status flint_ops_error_word(unsigned* out);
 
 #ifdef __cplusplus

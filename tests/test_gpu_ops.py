@@ -697,3 +697,10 @@ def test_no_rows_are_no_ops():
 
 def test_no_wait_has_given_up():
     assert B.flint_ops_error_word() == 0
+
+
+def test_error_word_of_each_way_to_ask():
+    d = block_inputs(12, seed=3)
+    ex = ops.FlintExperts16(d["gu"], d["dn"])
+    block_step(d, ex)
+    assert ops.error_word() == ops.error_word("cuda:0") == ops.error_word(torch.device("cuda", 0)) == ex.error_word() == 0

@@ -216,3 +216,12 @@ def test_wrappers_refuse_sizes_that_pass_32_bits(monkeypatch):
                  lambda: ops.block_norm(m(big, 1)), lambda: ops.block_norm(m(1, big))):
         with pytest.raises(ValueError, match="at most 2"):
             call()
+
+
+def test_error_word_is_the_asked_devices(monkeypatch):
+    asked = []
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext(asked.append(device)))
+    monkeypatch.setattr(ops.B, "flint_ops_error_word", lambda: 4)
+    ex = ops.FlintExperts16(torch.zeros((2, 4, 8)).as_subclass(_OnDevice), torch.zeros((2, 8, 2)).as_subclass(_OnDevice))
+    assert ops.error_word() == ops.error_word(1) == ex.error_word() == 4
+    assert asked == [None, 1, torch.device("cuda", 0)]
