@@ -325,6 +325,29 @@ def test_grouped_large_groups(act, gather):
     grouped_check([1030], 6000, 72, torch.float16, act, 12, gather=gather)
 
 
+def two_blocks(counts, N, act, sms):
+    """Whether gathered rows in these groups go to the kernel with two blocks of weights per tile (csrc/grouped.cu)."""
+    P, E, nout = sum(counts), len(counts), N // 2 if act else N
+    wide = -(-nout // (128 if act else 256))
+    return P // E > 128 and 2 * wide * max(P // 256, E) >= 3 * sms
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("over", [1, 100, 127, 128, 129, 200, 256])
+def test_grouped_two_blocks_of_weights(over, act, dtype):
+    # uneven groups (an empty one, one that ends inside a tile) and outputs that end `over` behind a tile's start: inside its
+    # first block, on the blocks' border, inside the second one
+    counts = [300, 0, 257, 513, 40, 129]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    step = 128 if act else 256                       # outputs of a tile
+    tiles = -(-3 * sms // (2 * len(counts)))
+    nout = (tiles - 1) * step + (over + 1) // (2 if act else 1)
+    N = 2 * nout if act else nout
+    assert two_blocks(counts, N, act, sms)
+    grouped_check(counts, N, 72 if over % 2 else 136, dtype, act, over, gather=True, pad=8, row_div=1 + over % 3)
+
+
 def test_grouped_many_experts_and_odd_widths():
     rng = np.random.default_rng(0)
     counts = rng.integers(0, 4, 1024)
