@@ -258,6 +258,103 @@ def test_q4_rotated_fp16_keeps_the_outputs_rounding(N, K, T):
     assert got <= (1 + 4 / np.sqrt(ref.size)) * least + (2.0 ** -13 * np.linalg.norm(ref)) ** 2, (got, least)
 
 
+def ring_form(fmt, N, K, T, sms):
+    """(blocks a team takes at a time, rounds, whether x comes through the ring, whether the scales stay in shared memory) of
+    the product for up to 8 tokens (csrc/q4_linear.cu)."""
+    segs, per = -(-K // 128), -(-N // sms)
+    b16 = -(-per // 16)
+    kw = 1
+    while kw < segs and kw < (16 if b16 == 1 else 8):
+        kw *= 2
+    teams = 16 // kw
+    rb = 1 if b16 <= teams else 2
+    blocks = -(-b16 // (teams * rb)) * teams * rb
+    scale_row = K // 64 if fmt == "int4" else K // 16
+    rows = -(-per // blocks) * blocks
+    tma = K % 32 == 0
+    return rb, blocks // (teams * rb), tma and T * segs > 64, tma and scale_row % 16 == 0 and rows * scale_row <= 72 * 1024
+
+
+LARGE = [("int4", True, 5001, 1024, 8, (2, 1, False, True)), ("int4", True, 5001, 4096, 8, (2, 1, True, True)),
+         ("int4", False, 8192, 1152, 8, (2, 1, True, False)), ("int4", True, 20001, 1024, 3, (2, 3, False, True)),
+         ("int4", True, 20001, 1152, 8, (2, 3, True, False)), ("int4", False, 20001, 2048, 5, (2, 3, True, True)),
+         ("nvfp4", False, 5001, 1152, 8, (2, 1, True, False)), ("nvfp4", False, 9600, 4112, 2, (2, 2, False, False)),
+         ("nvfp4", False, 8192, 4112, 8, (2, 1, False, False)), ("nvfp4", False, 20001, 1280, 8, (2, 3, True, True)),
+         ("nvfp4", False, 10001, 1040, 7, (2, 2, False, False)), ("nvfp4", False, 12001, 2048, 8, (2, 2, True, True)),
+         ("int4", True, 2368, 16384, 1, (1, 1, True, True)), ("int4", True, 9600, 8192, 8, (2, 2, True, True))]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("i", range(len(LARGE)))
+def test_q4_few_tokens_many_rows(i, dtype):
+    # two blocks of rows per team, one to three rounds that end inside the last, the operand built by every CTA or brought
+    # through the ring, scales kept in shared memory or read when needed
+    fmt, rotated, N, K, T, form = LARGE[i]
+    if torch.cuda.get_device_properties(0).multi_processor_count == 148:
+        assert ring_form(fmt, N, K, T, 148) == form
+    x, codes, scales, ts = q4_case(fmt, N, K, T, dtype, N + K + T, pad=8 * (i % 2))
+    y = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=rotated)
+    ref, slack = q4_reference(x, codes, scales, ts, fmt, rotated)
+    close(y, ref, dtype, slack, 2.0 ** -11 if rotated else 0.0)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
+@pytest.mark.parametrize("T,N,K", [(2, 96, 256), (8, 5001, 1024), (12, 96, 256), (40, 515, 1152)])
+def test_q4_extreme_activations_at_any_token_count(fmt, T, N, K):
+    # as above, for both formats and on both sides of eight tokens
+    x, codes, scales, ts = q4_case(fmt, N, K, T, torch.bfloat16, T, hot=False)
+    x = x.clone()
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    kinds = {"zero": 2, "inf": 3, "nan": 4} if T > 4 else {}
+    if kinds:
+        x[2] = 0
+        x[3, K - 7] = float("-inf")
+        x[4, 200] = float("nan")
+        codes = codes.clone()
+        at = (K - 7) // 2                                    # K - 7 is odd: the high nibble, code 3 against the infinity
+        codes[:, at] = (codes[:, at] & 0x0F) | 0x30
+        if fmt == "nvfp4":                                       # and no scale of zero against it
+            b = scales.view(torch.uint8).clone()
+            b[:, (K - 7) // 16] = b[:, (K - 7) // 16].clamp(min=0x20)
+            scales = b.view(torch.float8_e4m3fn)
+    keep = [t for t in range(T) if t not in (kinds.get("inf"), kinds.get("nan"))]
+    for rotated in ((False, True) if fmt == "int4" else (False,)):
+        y = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=rotated)
+        ref, slack = q4_reference(x[keep], codes, scales, ts, fmt, rotated)
+        got = y[keep]
+        order = np.argsort([0 if t == 0 else 1 if t == 1 else 2 for t in keep], kind="stable")
+        for part in (order[:1], order[1:2], order[2:]):          # a norm bound for each magnitude
+            if len(part):
+                close(got[part.tolist()], ref[part], torch.bfloat16, slack[part], 2.0 ** -11)
+        if kinds:
+            assert torch.all(y[2] == 0) and torch.isnan(y[4]).all() and not torch.isfinite(y[3]).any()
+            if not rotated:
+                sign = scales.float()[:, 0 if fmt != "int4" else (K - 7) // 128] if fmt == "int4" else torch.ones(N, device="cuda")
+                assert torch.equal(y[3] < 0, sign > 0) and torch.isinf(y[3]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
+def test_q4_every_code_and_scale_is_exact_in_small_batches(fmt):
+    # the test of 15 one-hot rows above, through the kernel for up to 8 tokens
+    K = 128
+    codes = torch.arange(256, dtype=torch.uint8).repeat(K // 2, 1).t().contiguous().cuda()
+    if fmt == "int4":
+        vals = [2.0 ** -20, 2.0 ** -130, 1.0, 255.0, -3.0, 1.5 * 2.0 ** 100, 0.0, 0.0039]
+        scales = torch.tensor(vals, dtype=torch.float32).to(torch.bfloat16).repeat(32)[:, None].contiguous().cuda()
+        ts = None
+    else:
+        scales = torch.arange(256 * 8, dtype=torch.int64).remainder(256).to(torch.uint8)
+        scales[(scales & 0x7F) == 0x7F] = 0x38
+        scales = scales.reshape(256, 8).view(torch.float8_e4m3fn).cuda()
+        ts = torch.ones(1).cuda()
+    for rows in (torch.arange(0, 8), torch.arange(60, 68), torch.arange(3, 128, 25)):
+        x = torch.eye(K)[rows].contiguous().to(torch.bfloat16).cuda()
+        y = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=False)
+        ref, _ = q4_reference(x, codes, scales, ts, fmt, False)
+        np.testing.assert_array_equal(f64(y), f64(torch.from_numpy(ref).to(torch.bfloat16)))
+
+
 # ------------------------------------------------------------------------------------------ grouped linear
 
 def counts_to_offsets(counts):
