@@ -119,8 +119,9 @@ __device__ __forceinline__ void load8_weight(const void* w, int w_f32, int v, in
   else widen8<TYPE>(load8<VEC>(static_cast<const uint16_t*>(w), v, H), out);
 }
 
-// 1 / (1 + e^-g) by the approximate base-2 exponential and reciprocal: within (|g| + 4) 2^-24 of itself, and 0 where e^-g passes
-// 2^126
+// 1 / (1 + e^-g) by the approximate base-2 exponential and reciprocal: within (1.3 |g| + 7) 2^-24 of itself. The argument's
+// rounding and that of log2 e take 1.23 |g|, the exponential (2^-22) 4, the sum 1 and the reciprocal (2^-23) 2. It is 0 where
+// e^-g passes 2^126.
 __device__ __forceinline__ float sigmoid_fast(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

@@ -664,6 +664,26 @@ def test_block_norm_of_values_whose_squares_pass_fp32(T, H):
     assert torch.isnan(z[0, 0]) and torch.all(z[0, 1:] == 0) and torch.isnan(z[1]).all() and torch.isfinite(z[2]).all()
 
 
+def test_block_norm_gate_at_any_size():
+    # sigmoid of every bf16 gate value, seen through an fp32 residual: x' = sigmoid(g) b with b = 1. The bound is the one
+    # stated at the kernel's sigmoid, (1.3 |g| + 7) 2^-24 of the value, plus half a step of the fp32 product; values below
+    # fp32's normal range may be flushed to zero.
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16)
+    g = bits[torch.isfinite(bits.float())]
+    g = torch.cat((g, g[:(-g.numel()) % 8])).reshape(1, -1)[:, :32768]
+    rest = bits[torch.isfinite(bits.float())][32768:].reshape(1, -1)
+    for gate in (g, rest):
+        H = gate.shape[1]
+        xo, _ = ops.block_norm(torch.zeros((1, H), device="cuda"), torch.ones((1, H), dtype=torch.bfloat16, device="cuda"),
+                               gate=gate.cuda(), gate_act="sigmoid")
+        gd = f64(gate)
+        with np.errstate(over="ignore"):
+            ref = 1 / (1 + np.exp(-gd))
+        tol = ref * ((1.3 * np.abs(gd) + 7) * 2.0 ** -24 + 2.0 ** -24) + 2.0 ** -126
+        err = np.abs(f64(xo) - ref)
+        assert np.all(err <= np.where(np.isfinite(tol), tol, 2.0 ** -126)), float((err / tol).max())
+
+
 # ------------------------------------------------------------------------------------------- used together
 
 def block_inputs(T, H=256, I=128, E=16, k=4, seed=0):
