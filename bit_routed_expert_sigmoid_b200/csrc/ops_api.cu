@@ -102,7 +102,8 @@ flint_status flint_expert_permute(const int* ids, int T, int top_k, int E, int* 
   if (top_k > kMaxOpTopK || E > kMaxOpGroups || static_cast<long long>(T) * top_k > kMaxOpPairs) return FLINT_ERR_UNSUPPORTED;
   if (!aligned_to(offsets, 4)) return FLINT_ERR_INVALID_ARG;
   if (T > 0 && (!aligned_to(ids, 4) || !aligned_to(perm, 4) || !aligned_to(inv, 4))) return FLINT_ERR_INVALID_ARG;
-  if (T > 0 && (perm == inv || ids == perm || ids == inv || ids == offsets)) return FLINT_ERR_INVALID_ARG;
+  if (T > 0 && (perm == inv || offsets == perm || offsets == inv || ids == perm || ids == inv || ids == offsets))
+    return FLINT_ERR_INVALID_ARG;
   return status_of(launch_expert_permute(ids, T * top_k, E, offsets, perm, inv, static_cast<cudaStream_t>(stream)));
 }
 

@@ -225,3 +225,8 @@ def test_error_word_is_the_asked_devices(monkeypatch):
     ex = ops.FlintExperts16(torch.zeros((2, 4, 8)).as_subclass(_OnDevice), torch.zeros((2, 8, 2)).as_subclass(_OnDevice))
     assert ops.error_word() == ops.error_word(1) == ex.error_word() == 4
     assert asked == [None, 1, torch.device("cuda", 0)]
+
+
+@pytest.mark.parametrize("kw", [dict(perm=C), dict(inv=C)])
+def test_permute_refuses_offsets_that_are_another_output(kw):
+    assert _status("flint_expert_permute", PE, **kw) == INVALID
