@@ -267,6 +267,8 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, post_norm: boo
     dt = y.dtype if y is not None else z.dtype if z is not None else z_dtype or (
         xt if xt in _TYPES else torch.bfloat16)
     t, act = _TYPES.get(dt), _GATES.get(gate_act)
+    if z_dtype is not None and z_dtype != dt:
+        raise ValueError(f"z_dtype {z_dtype} where the branch or z is {dt}")
     if t is None or act is None or (xt != torch.float32 and xt != dt):
         raise ValueError(f"a {xt} residual with a {dt} branch, gate_act {gate_act!r}")
     py = ldy = pg = ldg = 0

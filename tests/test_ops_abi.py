@@ -230,3 +230,16 @@ def test_error_word_is_the_asked_devices(monkeypatch):
 @pytest.mark.parametrize("kw", [dict(perm=C), dict(inv=C)])
 def test_permute_refuses_offsets_that_are_another_output(kw):
     assert _status("flint_expert_permute", PE, **kw) == INVALID
+
+
+def test_block_norm_refuses_another_type_for_z_than_the_branchs(monkeypatch):
+    monkeypatch.setattr(ops, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(ops, "_stream_of", lambda index: 0)
+    monkeypatch.setattr(ops.B, "flint_block_norm", lambda *a: None)
+    x, b, h = torch.zeros((2, 8)), torch.zeros((2, 8), dtype=torch.bfloat16), torch.zeros((2, 8), dtype=torch.float16)
+    with pytest.raises(ValueError, match="z_dtype"):
+        ops.block_norm(x, b, z_dtype=torch.float16)
+    with pytest.raises(ValueError, match="z_dtype"):
+        ops.block_norm(x, z=h, z_dtype=torch.bfloat16)
+    assert ops.block_norm(x, b, z_dtype=torch.bfloat16)[1].dtype == torch.bfloat16
+    assert ops.block_norm(x, z_dtype=torch.float16)[1].dtype == ops.block_norm(x, z=h)[1].dtype == torch.float16
