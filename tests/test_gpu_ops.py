@@ -8,6 +8,10 @@ Rotated activations are rounded once to 16 bits of at least fp16's precision per
 more. Over a whole output the roundings are independent, so the error's norm stays below (u_t + 2^-11 if rotated)
 times the result's norm, a bound that a wrong element or group breaks at once."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -682,6 +686,114 @@ def test_block_norm_gate_at_any_size():
         tol = ref * ((1.3 * np.abs(gd) + 7) * 2.0 ** -24 + 2.0 ** -24) + 2.0 ** -126
         err = np.abs(f64(xo) - ref)
         assert np.all(err <= np.where(np.isfinite(tol), tol, 2.0 ** -126)), float((err / tol).max())
+
+
+# ---------------------------------------------------------------------------------- the ends of the ranges
+
+def test_q4_of_the_largest_token_count_and_of_many_rows():
+    for fmt, N, K, T in (("int4", 5, 128, 65536), ("nvfp4", 3, 48, 65536), ("int4", 400003, 128, 2), ("int4", 400003, 128, 9),
+                         ("nvfp4", 400003, 32, 8)):
+        x, codes, scales, ts = q4_case(fmt, N, K, T, torch.bfloat16, N + T)
+        y = ops.q4_linear(x, codes, scales, ts, fmt=fmt, rotated=fmt == "int4")
+        ref, slack = q4_reference(x, codes, scales, ts, fmt, fmt == "int4")
+        close(y, ref, torch.bfloat16, slack, 2.0 ** -11 if fmt == "int4" else 0.0)
+
+
+@pytest.mark.parametrize("T", [3, 20])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_q4_int4_with_a_tensor_scale(dtype, T):
+    x, codes, scales, _ = q4_case("int4", 130, 512, T, dtype, T, hot=False)
+    ts = torch.tensor([-0.37]).cuda()
+    for rotated in (True, False):
+        y = ops.q4_linear(x, codes, scales, ts, fmt="int4", rotated=rotated)
+        ref, slack = q4_reference(x, codes, scales, ts, "int4", rotated)
+        close(y, ref, dtype, np.abs(slack), 2.0 ** -11 if rotated else 0.0)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_grouped_of_several_hundred_thousand_rows(gather):
+    grouped_check([100001, 0, 200003, 7], 24, 16, torch.bfloat16, "swiglu", 3, gather=gather, tail=9, row_div=3)
+
+
+def test_permute_of_the_largest_batch():
+    T, k, E = 1 << 21, 2, 1024
+    g = torch.Generator().manual_seed(0)
+    ids = torch.randint(-20, E + 20, (T, k), generator=g, dtype=torch.int32)
+    off, perm, inv = ops.expert_permute(ids.cuda(), E)
+    flat = ids.reshape(-1).long().numpy()
+    key = np.where((flat < 0) | (flat >= E), E, flat)
+    order = np.argsort(key, kind="stable")
+    counts = np.bincount(key, minlength=E + 1)[:E]
+    kept = int(counts.sum())
+    np.testing.assert_array_equal(off.cpu().numpy(), np.concatenate([[0], np.cumsum(counts)]))
+    np.testing.assert_array_equal(perm.cpu().numpy(), np.where(np.arange(T * k) < kept, order, -1))
+    pos = np.empty(T * k, dtype=np.int64)
+    pos[order] = np.arange(T * k)
+    np.testing.assert_array_equal(inv.cpu().numpy().reshape(-1), np.where(key < E, pos, -1))
+
+
+def test_rows_behind_2_to_the_31_elements():
+    # offsets of rows that pass 32 bits: the last rows of large strided buffers, and the first ones beside them
+    bf = torch.bfloat16
+    wide = torch.empty((6, 1 << 29), dtype=bf, device="cuda")      # rows 2^29 elements apart, the last from 5 * 2^29 on
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((6, 512), generator=g).to(bf).cuda()
+    far = wide[:, :512]
+    far.copy_(x)
+    w = (torch.randn((2, 64, 512), generator=g) * 0.05).to(bf).cuda()
+    off = torch.tensor([0, 2, 6], dtype=torch.int32).cuda()
+    assert torch.equal(ops.grouped_linear(far, w, off), ops.grouped_linear(x, w, off))
+    rows = torch.tensor([5, 0, 4, 5, 3, 1] * 20, dtype=torch.int32).cuda()
+    off2 = torch.tensor([0, 50, 120], dtype=torch.int32).cuda()
+    assert torch.equal(ops.grouped_linear(far, w, off2, rows=rows), ops.grouped_linear(x, w, off2, rows=rows))
+    codes, scales, _ = ops.quantize_linear(w[0].contiguous(), fmt="int4")
+    assert torch.equal(ops.q4_linear(far, codes, scales), ops.q4_linear(x, codes, scales))
+    inv = torch.tensor([[5, 0], [4, -1], [3, 5]], dtype=torch.int32).cuda()
+    cw = torch.rand((3, 2), generator=g).cuda()
+    assert torch.equal(ops.expert_combine(far, inv, cw), ops.expert_combine(x, inv, cw))
+    want = ops.block_norm(x, x)
+    out = wide[:, 1024:1536], wide[:, 2048:2560]
+    got = ops.block_norm(far, far, x_out=out[0], z=out[1])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y = wide[:, 4096:4160]
+    ops.grouped_linear(x, w, off, y=y)
+    assert torch.equal(y, ops.grouped_linear(x, w, off))
+    del wide, far, out, got, y
+    torch.cuda.empty_cache()
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from bit_routed_expert_sigmoid_b200 import ops
+bf = torch.bfloat16
+e = lambda *s, dtype=bf: torch.ones(s, device="cuda").to(dtype)
+T = {T}
+x, y = e(T, 256, dtype=torch.float32), e(T, 256)
+codes, scales = e(64, 128, dtype=torch.uint8), e(64, 2)
+n_codes, n_scales, ts = e(64, 128, dtype=torch.uint8), e(64, 16, dtype=torch.uint8), e(1, dtype=torch.float32)
+gu, dn, ids, w = e(4, 64, 256), e(4, 256, 32), e(T, 2, dtype=torch.int32), e(T, 2, dtype=torch.float32)
+def step():
+    x1, z = ops.block_norm(x, y)
+    return (z, ops.q4_linear(z, codes, scales), ops.q4_linear(z, n_codes, n_scales, ts, fmt="nvfp4"),
+            ops.FlintExperts16(gu, dn).forward(z, ids, w, addend=y))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step())) and ops.error_word() == 0
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_the_first_call_of_a_process_may_be_captured(T):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root, T=T)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------------------------------- used together
