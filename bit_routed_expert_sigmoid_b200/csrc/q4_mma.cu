@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
   if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
+constexpr int kAlone = 115 * 1024;               // more than half of an SM's 228 KB
 constexpr int kMost = 226 * 1024 - static_cast<int>(sizeof(MmBars)) - kMmRing * 4 * kMmTokens - 256;
 
 // Clusters of k CTAs that the device runs at once: fewer than SMs / k, as a cluster stays within a group of SMs.
@@ -451,6 +452,9 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
   if (smem < parts) smem = parts;
   // the MMA reads N16 rows of the operand's last block, up to 8 more than there are
   if (smem < 1024 + kMmPairStages * b_stage + 1024) smem = 1024 + kMmPairStages * b_stage + 1024;
+  // One CTA per SM, whatever its registers: a second one would wait for the first one's tensor memory, and two clusters
+  // that share two SMs crosswise would wait for each other.
+  if (smem < kAlone) smem = kAlone;
   if (smem > kMost) return cudaErrorInvalidConfiguration;
   if (TMA && !(mp.boxed ? encode_words_blocks(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R, kMmChunk / 2)
                         : encode_words(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R)))
