@@ -2,7 +2,8 @@
 
 The layer runs in the CUDA library libflint_moe.so behind the C ABI in include/flint_moe.h;
 `binding` marshals arguments to it, `layer` keeps a layer's weights and workspace in PyTorch device
-memory, `synthetic` draws the seeded workloads.
+memory, `ops` offers the operators around it at any width (include/flint_ops.h), `synthetic` draws the
+seeded workloads.
 """
 
-__all__ = ["binding", "layer", "synthetic", "build"]
+__all__ = ["binding", "layer", "ops", "synthetic", "build"]
