@@ -54,8 +54,8 @@ EXPORTS = (
     "flint_moe_status_string", "flint_moe_set_stage_events", "flint_moe_stage_count", "flint_moe_stage_name",
     "flint_moe_route_noalloc", "flint_residual_rmsnorm", "flint_moe_stack_forward",
     "flint_quantize_int4_g128", "flint_quantize_nvfp4",
-    "flint_q4_linear", "flint_q4_linear_workspace_size", "flint_grouped_linear", "flint_expert_permute", "flint_expert_combine", "flint_block_norm",
-    "flint_ops_error_word",
+    "flint_q4_linear", "flint_q4_linear_workspace_size", "flint_grouped_linear", "flint_expert_permute",
+    "flint_expert_combine", "flint_block_norm", "flint_ops_error_word",
 )
 
 

@@ -8,7 +8,9 @@
 // ever written (TMA's gather4 measured ~70 cycles per four 128-byte rows: 4096^3 took 602 us with it). With few
 // rows per expert it is bound by streaming the weights once; with many, by the tensor cores.
 // grouped_few_kernel serves decode (P <= kFewRows): see there. 256 experts, gate|up 1024 x 2048: 12288 rows 160 us, 192
-// rows 91 (HBM 167 and 87 with a cold L2), 24 rows 21.4 (14.9); one group of 4096^3 105 us (tensor cores 82).
+// rows 91, 24 rows 21.4; one group of 4096^3 106 us (tensor cores 82). These, and all times in this file, are of calls in a
+// CUDA graph, where up to 126 MB of the weights are still in L2; with L2 flushed, and the launch included, 180, 104 and 28.0
+// (once through HBM 167, 87, 14.9).
 #include "kernels.cuh"
 #include "ops.cuh"
 #include "tc.cuh"
@@ -21,14 +23,17 @@ __device__ unsigned g_ops_error;                 // timeout bits of bounded wait
 namespace {
 
 constexpr int kGrMaxE = 1024;
-constexpr int kGrThreads = 384;                  // copies: 2 warps, MMA: 1, idle: 1, epilogue: 8; and 4 more that gather rows
+constexpr int kGrThreads = 384;                  // copies: 2 warps, MMA: 1, idle: 1, epilogue: 8; and 4 more that gather
 constexpr int kGrTabWarps = 8;                   // warps that build the tile table
 constexpr int kGrGather = 128;
 constexpr int kGrABytes = 128 * 128;             // a stage of weights: 128 rows x 64 K
 constexpr int kGrSlab = 2 * 2 * 16 * 64 * 4;      // SwiGLU: two teams x (gate, up) x 16 columns x 64 rows, fp32
 // Rows up to which grouped_few_kernel is taken: 24 rows over 256 experts take 21.4 us there and 26.6 by the GEMM, 30 rows
-// 25.1 and 26.7, 60 rows 44 and 38. Groups of more than eight rows on average go to the GEMM, as their weights would be
-// read once per eight (28 rows of two experts, 4096 x 4096: 24.5 us and 20.4).
+// 25.1 and 26.7, 60 rows 44 and 38. It reads a group's weights once per eight of its rows, so with more than eight rows on
+// average, counted in whole eights (P / 8 > E), the GEMM is taken: 28 rows of two experts, 4096 x 4096, 24.5 us and 20.4.
+// Where that leaves a second reading, it still wins for one expert (12 rows, 4096 x 4096: 15.8 and 19.8) and for small
+// matrices (20 rows of two, gate|up 1024 x 2048: 7.9 and 13.3), and loses for a few large ones (20 rows of two, 4096 x
+// 4096: 23.5 and 20.2).
 constexpr int kFewRows = 32;
 
 // First row and number of rows of group e; offsets clamped to [0, P].
@@ -130,7 +135,8 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int it)
 // Warp 0: weights by TMA. Warp 1: MMA issue. Warp 2: rows by TMA, or the last four warps gather them. Warps 4-7 and 8-11:
 // epilogue, of 32 columns in turn or of a block each. One block has two sets of accumulators, two blocks have one.
 template <int TYPE, int ACT, int NMAX, bool GATHER, int MB>
-__global__ void __launch_bounds__(kGrThreads + (GATHER ? kGrGather : 0), 1) grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
+__global__ void __launch_bounds__(kGrThreads + (GATHER ? kGrGather : 0), 1)
+    grouped_mma_kernel(const __grid_constant__ GroupedMmaParams mp) {
   using G = GrGeom<NMAX, MB>;
   const GroupedParams& p = mp.g;
   extern __shared__ uint8_t smem_raw[];
@@ -400,9 +406,9 @@ cudaError_t launch_mma(const GroupedParams& p, int dev, int sms, cudaStream_t s)
 // rows and their 8 up rows) and spread evenly over one CTA per SM, which a GEMM's 128-row tiles cannot do when a token has
 // six experts. One thread keeps a ring of stages full: a stage is up to 1024 K of the units that the 16 other warps work
 // on, in teams of eight or four warps per unit (fewer when K is short), one TMA box of up to 32 KB per unit (half a unit
-// with SwiGLU). A warp takes 128 K of a stage and multiplies with mma.sync m16n8k16; any order of K serves as long as both operands have it, so a lane reads 8 neighbouring K at
-// a time and x comes straight from global memory, through L1. A team's partial sums meet in shared memory and are
-// added in warp order; teams do not wait for one another.
+// with SwiGLU). A warp takes 128 K of a stage and multiplies with mma.sync m16n8k16; any order of K serves as long as both
+// operands have it, so a lane reads 8 neighbouring K at a time and x comes straight from global memory, through L1. A
+// team's partial sums meet in shared memory and are added in warp order; teams do not wait for one another.
 // Small copies starve it: bulk copies of one row (1 or 4 KB) and boxes of 2 KB all streamed ~11 bytes per cycle and
 // SM, boxes of 8 KB and more over twice that.
 constexpr int kFewWarps = 16;                    // consumers; one more warp copies

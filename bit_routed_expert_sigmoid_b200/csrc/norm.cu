@@ -1,6 +1,7 @@
 // The residual step around a block (flint_block_norm): post-norm of the branch, gate, residual add and the
 // next block's pre-norm in one pass, every row read once and held in registers between the two reductions. Bound by HBM:
-// 8192 x 4096 bf16 with a gate per element moves 336 MB in 58.0 us (5.8 TB/s); 2048 x 2048 with an fp32 residual 9.2 us.
+// 8192 x 4096 bf16 with a gate per element moves 336 MB in 58.0 us (5.8 TB/s); 2048 x 2048 with an fp32 residual 9.2 us
+// (calls in a CUDA graph on rotating inputs, of which up to 126 MB are still in L2; flushed 68.5 and 16.4, launch included).
 #include "kernels.cuh"
 #include "ops.cuh"
 
@@ -120,8 +121,8 @@ __device__ __forceinline__ void load8_weight(const void* w, int w_f32, int v, in
 }
 
 // 1 / (1 + e^-g) by the approximate base-2 exponential and reciprocal: within (1.3 |g| + 7) 2^-24 of itself. The argument's
-// rounding and that of log2 e take 1.23 |g|, the exponential (2^-22) 4, the sum 1 and the reciprocal (2^-23) 2. It is 0 where
-// e^-g passes 2^126.
+// rounding and that of log2 e take 1.23 |g|, the exponential (2^-22) 4, the sum 1 and the reciprocal (2^-23) 2. It is 0
+// where e^-g passes 2^126.
 __device__ __forceinline__ float sigmoid_fast(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

@@ -1,12 +1,17 @@
 // Linear products with 4-bit weights for few tokens (flint_q4_linear):
 //   y[t][n] = ts * sum over 128-segments of  s[n] * (code[n] . x'[t]),  x' = x or blockdiag(Hn) x.
 //
-// Up to 8 tokens (this file; more: q4_mma.cu) it is bound by streaming the weights once, and close behind by the
-// instructions that decode them: 8192 x 8192 int4 takes 15.4 us at T = 8 and 12.7 at T = 1 (HBM 5.3; a launch that only
-// reads the codes 8.3), NVFP4 22.8; T = 9 takes 20.1 in the other file.
-// The rows of W are divided evenly over one CTA per SM (not in units of a tile); the 16 warps of a CTA split K:
-// a warp takes a 128-segment of one or two blocks of up to 16 rows at a time, as fragments of mma.sync. A fragment's K order is free as long as x has the same: a lane's 16 bytes are 32 neighbouring K of one row.
-// The int4 group scale and the operand's factor (q4_operand.cuh) multiply the segment's sum in fp32.
+// Up to 8 tokens (this file; more: q4_mma.cu). 8192 x 8192 int4 takes 15.4 us at T = 8 and 13.1 at T = 1, NVFP4 22.8 at
+// T = 8; T = 9 takes 20.1 in the other file. These, and all times in this file, are of calls in a CUDA graph, whose weights
+// (36 MB here) stay in L2; with L2 flushed, and the launch included, 21.4, 19.6 and 29.2. Once through HBM the weights are
+// 5.3 us, and a launch that only reads the codes takes 8.3. Nothing is near saturated: at T = 8 40 % of the issue slots are
+// used, 25 % of DRAM, 13 % of the tensor pipe; a warp waits a third of its time for loads and stages (NVFP4: 54, 18 and 9 %,
+// and more for the arithmetic pipes that decode, and for its turn, than for loads).
+//
+// The rows of W are divided evenly over one CTA per SM (not in units of a tile); the 16 warps of a CTA split K: a warp
+// takes a 128-segment of one or two blocks of up to 16 rows at a time, as fragments of mma.sync. A fragment's K order is
+// free as long as x has the same: a lane's 16 bytes are 32 neighbouring K of one row. The int4 group scale and the operand's
+// factor (q4_operand.cuh) multiply the segment's sum in fp32.
 //
 // With few segments every CTA builds the operand itself in shared memory; with more, one kernel builds it once in the
 // workspace and the product kernel, launched behind it as a programmatic dependent, starts its weight copies meanwhile.

@@ -5,16 +5,18 @@
 // tiles of 111 rows, two CTAs each). Two teams of four warps take 128-segments in turn (8192 x 8192 at T = 16: one team
 // 23.5 us, two 21.6, four 24.0), a thread decoding one row's 128 codes to exact fp16; two warps issue the MMAs of a segment
 // in turn (an instruction takes ~45 cycles to issue), each into an accumulator of the segment's own; eight warps add the
-// accumulators, times the rows' group scales and the tokens' factors, to fp32 sums in registers: scales of any range and
-// tokens of any magnitude lose nothing. At the end the CTAs of a cluster exchange their sums through distributed shared
-// memory and add them in rank order.
+// accumulators, times the rows' group scales and the tokens' factors, to fp32 sums in registers, so that neither is rounded
+// to fp16. At the end the CTAs of a cluster exchange their sums through distributed shared memory and add them in rank order.
 // Codes come by TMA, 512 K of all rows per stage, the operand too, a pair of segments per stage (kF16Pair: the two parts of
 // one), with its factors; rows of codes that are no multiple of 16 bytes (K % 32 = 16) are read by the decoding warps.
-// 8192 x 8192 takes 20.1 us at T = 16 and 24.4 at T = 64, 5001 x 4112 NVFP4 15.6 at T = 37 (HBM 5.4, 5.6, 1.9). What bounds it
-// is the chain of a segment, 0.4 us a team: codes to registers, decoding, the store to tensor memory, eight MMAs, the
-// sums. More stages, more teams or codes released before they are decoded only made the warps wait for one another.
-// (With the tokens on the M side every MMA reads 128 operand rows from shared memory, 32 KB per segment whatever T is:
-// that took 46 us for 8192 x 8192.)
+//
+// 8192 x 8192 takes 20.3 us at T = 16 and 24.6 at T = 64, 5001 x 4112 NVFP4 15.6 at T = 37: calls in a CUDA graph, weights in
+// L2, as all times in this file; with L2 flushed and the launch included 26.3, 32.0 and 35 (once through HBM 5.4, 5.6, 1.9).
+// More than 64 tokens run in chunks that fetch and decode W again: 256 tokens 90 us, 2048 tokens 691 (tensor cores 20, 164).
+// What bounds it is the chain of a segment, 0.4 us a team: codes to registers, decoding, the store to tensor memory, eight
+// MMAs, the sums. 54 % of the issue slots are used; the warps wait for one another's results, and more stages, more teams or
+// codes released before they are decoded only made them wait longer. (With the tokens on the M side every MMA reads 128
+// operand rows from shared memory, 32 KB per segment whatever T is: that took 46 us for 8192 x 8192.)
 #include <limits.h>
 
 #include "kernels.cuh"
@@ -209,8 +211,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
         const uint32_t b0 = smem_u32(sm_b + sb * b_stage) + (kSegs == 2 ? w * TB * 256 : 0);
 #pragma unroll
         for (int ks = 0; ks < 8 * kParts<AR>; ++ks)
-          tc_mma_ta_w(tmem + sd * 64, tmem_a + sa * 64 + (ks & 7) * 8, sdesc_sw128(b0 + (ks >> 2) * TB * 128 + (ks & 3) * 32), idesc,
-                      ks ? 1u : 0u);
+          tc_mma_ta_w(tmem + sd * 64, tmem_a + sa * 64 + (ks & 7) * 8, sdesc_sw128(b0 + (ks >> 2) * TB * 128 + (ks & 3) * 32),
+                      idesc, ks ? 1u : 0u);
         tc_commit_w(&bb.a_empty[sa]);
         tc_commit_w(&bb.d_full[sd]);
       }
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q4_mma_kernel(const __grid_cons
     tc_commit_w(&bb.done[w]);
     pf_wait_all(&bb.done[w], 0, abort, err);
   } else if (warp < kMmSums) {
-    // ---- decoding: a thread per row, 128 codes of every fourth segment
+    // ---- decoding: a thread per row, 128 codes of every kMmTeams-th segment
     const int team = (warp - 4) >> 2, row = 32 * (warp & 3) + lane;
     const int n = min(row0 + min(row, R - 1), p.N - 1);
     const uint32_t lane_base = tmem_a + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -459,7 +461,8 @@ cudaError_t launch_mm(const Q4Params& p, cudaStream_t s) {
   if (TMA && !(mp.boxed ? encode_words_blocks(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R, kMmChunk / 2)
                         : encode_words(&mp.tm_codes, p.codes, p.N, p.K / 2, mp.R)))
     return cudaErrorInvalidValue;
-  if (mp.scale_row && !encode_words_rows(&mp.tm_scales, p.scales, p.N, scale_row, mp.scale_row, mp.R)) return cudaErrorInvalidValue;
+  if (mp.scale_row && !encode_words_rows(&mp.tm_scales, p.scales, p.N, scale_row, mp.scale_row, mp.R))
+    return cudaErrorInvalidValue;
   const uint64_t cols = static_cast<uint64_t>(segs) * 128 * kParts<AR>;
   if (!encode_16bit_blocks(&mp.tm_x, p.workspace, false, p.T, cols, cols, mp.TB, 4))
     return cudaErrorInvalidValue;

@@ -14,10 +14,10 @@ namespace {
 //              2^15): 16-bit inputs stay exact down to 2^-29 of it (2^-38 absolute). The factor is taken out of the fp32 sum
 //              again. Rotated bf16 inputs are rounded to fp16's 11 bits, an eighth of the output's rounding: 2.0e-4 of the
 //              result's norm beside 1.66e-3.
-//   kF16Pair   rotated int4 of fp16 inputs, more tokens: there the same rounding would be as large as the output's (2.9e-4 of
-//              the norm in all against 2.07e-4), so Hn x enters as the sum of two fp16 numbers, 22 bits, at twice the MMAs:
-//              8192 x 8192 takes 24.9 us at T = 16 and 30.2 at T = 64, where one number takes 20.3 and 24.6. Six stages of the
-//              operand instead of three: 26.5 and 33.6. An infinity's second part is NaN.
+//   kF16Pair   rotated int4 of fp16 inputs, more tokens: there the same rounding would be as large as the output's (2.9e-4
+//              of the norm in all against 2.07e-4), so Hn x enters as the sum of two fp16 numbers, 22 bits, at twice the
+//              MMAs: 8192 x 8192 takes 24.8 us at T = 16 and 30.1 at T = 64, where one number takes 20.3 and 24.6 (warm L2).
+//              Six stages of the operand instead of three: 26.5 and 33.6. An infinity's second part is NaN.
 //   kLimbs     rotated int4, few tokens: Hn x is rounded to 16-bit fixed point per (token, segment), a unit being 2^-14
 //              of the power of two below the segment's largest value (rotation spreads outliers, so that is finer than
 //              fp16 for all but the smallest values); its signed high and unsigned low bytes multiply the exact int8
@@ -37,7 +37,9 @@ constexpr int kParts = AR == kF16Pair ? 2 : 1;
 enum OperandLayout : int { kTokens, kRows };
 constexpr int kTokenBytes = 272;
 
-__host__ __device__ inline size_t q4_rows_factors(int T, int segs, int parts) { return static_cast<size_t>(T) * segs * parts * 256; }
+__host__ __device__ inline size_t q4_rows_factors(int T, int segs, int parts) {
+  return static_cast<size_t>(T) * segs * parts * 256;
+}
 // of the form that takes most (more than 8 tokens: two parts)
 __host__ __device__ inline size_t q4_operand_bytes(int T, int segs) {
   return T <= 8 ? static_cast<size_t>(T) * segs * kTokenBytes
@@ -60,7 +62,8 @@ __device__ __forceinline__ OperandPlace q4_place(uint8_t* img, int t, int seg, i
   } else {
     o.at = img + (static_cast<size_t>(t) * segs + seg) * (256 * PARTS);
     o.chunk = 16, o.lane = 64;
-    o.factor = reinterpret_cast<float*>(img + q4_rows_factors(T, segs, PARTS)) + static_cast<size_t>(seg) * ((T + 3) & ~3) + t;
+    o.factor = reinterpret_cast<float*>(img + q4_rows_factors(T, segs, PARTS)) + static_cast<size_t>(seg) * ((T + 3) & ~3) +
+               t;
   }
   return o;
 }
@@ -161,7 +164,8 @@ __device__ __forceinline__ void q4_operand(const uint2 (&raw)[NP], bool rotate, 
         auto pairs = [&](const float (&w)[4]) {
           const float r0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[0] : w[2], 1);
           const float r1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[1] : w[3], 1);
-          return odd ? make_uint2(pack_half2(r0, w[2]), pack_half2(r1, w[3])) : make_uint2(pack_half2(w[0], r0), pack_half2(w[1], r1));
+          return odd ? make_uint2(pack_half2(r0, w[2]), pack_half2(r1, w[3]))
+                     : make_uint2(pack_half2(w[0], r0), pack_half2(w[1], r1));
         };
         u = pairs(v[j]);
         if constexpr (AR == kF16Pair) {
@@ -205,8 +209,8 @@ __global__ void __launch_bounds__(256) q4_operand_kernel(const __grid_constant__
 template <int AR, int TYPE, int LAYOUT>
 cudaError_t launch_q4_operand(const Q4Params& p, int sms, cudaStream_t s) {
   const long long pairs = static_cast<long long>(p.T) * ((p.K + 127) / 128), ctas = (pairs + 7) / 8;
-  return launch_pdl_kernel(q4_operand_kernel<AR, TYPE, LAYOUT>, static_cast<int>(ctas < 8 * sms ? ctas : 8 * sms), 256, 0, false,
-                           s, p);
+  const int grid = static_cast<int>(ctas < 8 * sms ? ctas : 8 * sms);
+  return launch_pdl_kernel(q4_operand_kernel<AR, TYPE, LAYOUT>, grid, 256, 0, false, s, p);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -4,7 +4,7 @@ As in `layer`, PyTorch supplies device memory and streams only; every step runs 
 kernels. Shapes, types and strides are checked here (ValueError) or by the C entry points (FlintError).
 Outputs that are not given are allocated; no gradients are recorded. Work goes to `stream` (default: the current stream of
 the inputs' device); an input written on another stream must have been ordered before it by the caller. With `stream`, the
-call's tensors are recorded on it, so that they may be dropped as soon as the call returns, and allocated outputs belong to it.
+call's tensors are recorded on it, so that they may be dropped as soon as the call returns; allocated outputs belong to it.
 
 Waits inside the kernels are bounded. Should one give up, its call's output is incomplete and `error_word` says so.
 

@@ -38,6 +38,8 @@ extern "C" {
  * Rounding before the sums: rotated activations, per (token, 128-segment), to 16-bit fixed point of the segment's
  * largest value (T <= 8) or, scaled by a power of two, to fp16's 11 bits (T > 8, BF16) or 22 bits (T > 8, F16). Unrotated
  * ones, and the codes times NVFP4's block scales, enter exactly, but for activations below 2^-29 of their segment's largest.
+ * A group scale times the segment's largest activation is formed in fp32 at 2^-18 of its size: between 2^-100 and 2^127 that
+ * loses nothing.
  * workspace: flint_q4_linear_workspace_size(K, T) bytes of device memory (the activations as the kernel's operand),
  * 256-byte aligned, in use until the call's work is done; may be NULL when that size is 0, as it is for the smallest
  * calls. The size is 0 for invalid arguments too. */
