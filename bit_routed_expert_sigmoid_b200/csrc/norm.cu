@@ -25,14 +25,14 @@ __device__ __forceinline__ float block_sum(float v, float* wsum) {
 
 // 1 / sqrt(mean + eps) over the row, from the thread's sum of squares. Values from 2^56 on may have a sum that passes
 // fp32's range: all threads of the CTA then see it infinite and add the squares of 2^-80 times the values (`scaled`), at
-// most 32768 of 2^96, beside which eps is nothing. An infinite or NaN value stays what it is.
+// most 32768 of 2^96. An infinite or NaN value stays what it is.
 template <bool WIDE, typename Scaled>
 __device__ __forceinline__ float inv_rms(float s, int H, float eps, float* wsum, Scaled scaled) {
   const float sum = block_sum(s, wsum);
   if constexpr (WIDE) {
     if (sum > 3.402823466e38f) {
       __syncthreads();                           // wsum is written again
-      return 0x1p-80f / sqrtf(block_sum(scaled(), wsum) / static_cast<float>(H));
+      return 0x1p-80f / sqrtf(block_sum(scaled(), wsum) / static_cast<float>(H) + eps * 0x1p-80f * 0x1p-80f);
     }
   }
   return 1.0f / sqrtf(sum / static_cast<float>(H) + eps);
