@@ -4,7 +4,8 @@ PyTorch only allocates device memory and provides streams here; every step of th
 the library's CUDA kernels (binding.flint_moe_forward).
 
 A call with `stream` records its tensors on that stream (and the layer its own memory), so that they may be dropped as soon
-as it returns; an allocated output belongs to `stream`. Inputs written on another stream are ordered before it by the caller.
+as it returns. An allocated output belongs to `stream` and is recorded on the caller's stream, which reads it when it has been
+ordered behind the call. Inputs written on another stream are ordered before it by the caller.
 """
 
 from __future__ import annotations
@@ -99,8 +100,13 @@ class FlintMoELayer:
             self._recorded.add(stream)
 
     def _output(self, T: int, stream) -> torch.Tensor:
-        with torch.cuda.stream(stream):          # of the current stream when None
+        if stream is None:
             return torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+        caller = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+        y.record_stream(caller)
+        return y
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: [T][H] bf16 (or int16 bit patterns) on the device. Returns y [T][H] bf16."""

@@ -4,7 +4,8 @@ As in `layer`, PyTorch supplies device memory and streams only; every step runs 
 kernels. Shapes, types and strides are checked here (ValueError) or by the C entry points (FlintError).
 Outputs that are not given are allocated; no gradients are recorded. Work goes to `stream` (default: the current stream of
 the inputs' device); an input written on another stream must have been ordered before it by the caller. With `stream`, the
-call's tensors are recorded on it, so that they may be dropped as soon as the call returns; allocated outputs belong to it.
+call's tensors are recorded on it, so that they may be dropped as soon as the call returns. Allocated outputs belong to it,
+and are recorded on the caller's stream, which reads them when it has been ordered behind the call.
 
 Waits inside the kernels are bounded. Should one give up, its call's output is incomplete and `error_word` says so.
 
@@ -43,7 +44,7 @@ def _elsewhere(device, stream) -> bool:
 def _used_on(stream, *values) -> None:
     """The memory of the tensors among `values` is not handed out again before the work that `stream` then holds is done."""
     for v in values:
-        if isinstance(v, torch.Tensor) and v.device.type == "cuda":
+        if isinstance(v, torch.Tensor) and v.device == stream.device:
             v.record_stream(stream)
 
 
@@ -55,9 +56,12 @@ def _switched(fn, device, stream, *args, **kw):
         with torch.cuda.device(device):
             return fn(*args, **kw)
     _need(stream.device == device, "the stream belongs to another device than the tensors")
+    caller = torch.cuda.current_stream(device)
     try:
         with torch.cuda.stream(stream):
-            return fn(*args, **kw)
+            out = fn(*args, **kw)
+        _used_on(caller, *(out if isinstance(out, tuple) else (out,)))
+        return out
     finally:
         _used_on(stream, *args, *kw.values())
 

@@ -904,7 +904,7 @@ def test_inputs_may_be_dropped_while_another_stream_still_reads_them():
         s.wait_stream(torch.cuda.current_stream())
         torch.cuda.synchronize()
         with torch.cuda.stream(s):
-            torch.cuda._sleep(100_000_000)           # about 50 ms
+            torch.cuda._sleep(1_000_000_000)         # about 0.5 s
         got = steps(d, ex, s)
         shapes = [(t.shape, t.dtype) for k, v in d.items() for t in (v if isinstance(v, tuple) else (v,)) if t is not None]
         del d, ex
@@ -915,6 +915,27 @@ def test_inputs_may_be_dropped_while_another_stream_still_reads_them():
             if j == 4:                               # rows of no expert are not written
                 a, b = a[:live], b[:live]
             assert torch.equal(a, b)
+        del over
+
+
+def test_allocated_outputs_may_be_dropped_while_the_caller_still_reads_them():
+    # the output is the given stream's memory: dropped by the caller, it must outlive what the caller's stream still does
+    d = block_inputs(24, seed=50)
+    want = ops.q4_linear(d["y"], *d["q"], fmt="int4").clone()
+    s = torch.cuda.Stream()
+    for _ in range(2):
+        s.wait_stream(torch.cuda.current_stream())
+        y = ops.q4_linear(d["y"], *d["q"], fmt="int4", stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(1_000_000_000)             # about 0.5 s
+        got = y.clone()
+        shape = y.shape
+        del y
+        with torch.cuda.stream(s):
+            over = [torch.full(shape, 77, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        assert not torch.cuda.current_stream().query()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
         del over
 
 

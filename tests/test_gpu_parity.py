@@ -321,7 +321,7 @@ def test_tensors_and_layer_may_be_dropped_while_another_stream_works(T):
     s.wait_stream(torch.cuda.current_stream())
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
-        torch.cuda._sleep(400_000_000)               # about 0.2 s
+        torch.cuda._sleep(1_000_000_000)             # about 0.5 s
     y = dev.forward(dx, stream=s)
     keep = dev.handle                                # destroyed by close() below, behind the work
     dev.tensors, dev.workspace, dx = {}, None, None

@@ -18,6 +18,9 @@ class _Stream:
     cuda_stream = 7
 
 
+_CALLER = _Stream()
+
+
 def _tensor(*shape):
     return torch.zeros(shape or (2, LY.H)).as_subclass(_Noted)
 
@@ -27,6 +30,7 @@ def bare(monkeypatch):
     """A layer without a handle, whose forwards launch nothing."""
     made = []
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext(made.append(s)))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: _CALLER)
     for name in ("flint_moe_forward", "flint_moe_forward_routed", "flint_moe_stack_forward"):
         monkeypatch.setattr(LY.B, name, lambda *a: None)
     one = object.__new__(LY.FlintMoELayer)
@@ -48,10 +52,12 @@ def test_a_forward_on_a_stream_records_what_it_uses(bare):
 
 
 def test_an_allocated_output_belongs_to_the_stream(bare, monkeypatch):
-    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, stream: None)      # the output is an ordinary host tensor here
+    # it is an ordinary host tensor here
+    monkeypatch.setattr(torch.Tensor, "record_stream", _Noted.record_stream)
     s = _Stream()
-    assert bare.forward(_tensor(), stream=s).shape == (2, LY.H)
-    assert bare.allocated_on == [s]
+    y = bare.forward(_tensor(), stream=s)
+    assert y.shape == (2, LY.H) and bare.allocated_on == [s] and y.streams == [_CALLER, s]
+    assert not hasattr(bare.forward(_tensor()), "streams") and bare.allocated_on == [s]
 
 
 def test_a_stack_on_a_stream_records_all_its_memory(bare):

@@ -170,11 +170,17 @@ class _OnDevice(torch.Tensor):
 
 def test_tensors_of_a_call_on_another_stream_are_recorded_there(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    caller = types.SimpleNamespace(device=torch.device("cuda", 0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: caller)
     monkeypatch.setattr(ops, "_current_device", lambda: 0)
     stream = types.SimpleNamespace(device=torch.device("cuda", 0))
     a, b, c, d = (torch.zeros(1).as_subclass(_OnDevice) for _ in range(4))
-    assert ops._switched(lambda x, k, z=None, f=0: x, a.device, stream, a, 3, z=b, f=1.5) is a
+    out = torch.zeros(1).as_subclass(_OnDevice), torch.zeros(1).as_subclass(_OnDevice)
+    assert ops._switched(lambda x, k, z=None, f=0: out, a.device, stream, a, 3, z=b, f=1.5) is out
     assert a.streams == b.streams == [stream]
+    # what the call allocated is the stream's own, and the caller's to read
+    assert out[0].streams == out[1].streams == [caller]
+    assert ops._switched(lambda x: out[0], a.device, stream, a) is out[0] and out[0].streams == [caller, caller]
 
     def fails(x, y):
         raise ValueError("refused behind a launch")
